@@ -2,7 +2,9 @@
  * orthoupd.h -- C ABI of liborthoupd.so: the optimizer step that
  * orthonormalizes each weight matrix's momentum (Muon Newton-Schulz, Gram
  * Newton-Schulz, the Dion3 row-selection rule, Dion / Orth-Dion low-rank
- * steps), as hand-written CUDA kernels for NVIDIA B200 (sm_100a).
+ * steps), as hand-written CUDA kernels for NVIDIA B200 (sm_100a); and the
+ * operators of the training step around it (8-bit products, norm,
+ * distillation loss).
  *
  * Sources the calls follow (cited by page title and section):
  *   [D3]  "Dion3: Full-Stack Orthogonal Updates" (arXiv abstract).
@@ -69,6 +71,10 @@ extern "C" {
 /* element types */
 #define OUO_F32 0
 #define OUO_BF16 1
+
+/* limits of the token-matrix calls */
+#define OUO_INT8_MAX_DEPTH 131071     /* int8_matmul: depth whose sums fit in 32 bits */
+#define OUO_DISTILL_MAX_ENTRIES 1024  /* distill_loss: teacher entries of a row        */
 
 /* momentum modes */
 #define OUO_MOMENTUM_EMA 0        /* M <- mu * M + G                         */
@@ -408,6 +414,115 @@ int dion_shard_update(const ouo_mat* M, const ouo_mat* Q_state,
                       const ouo_dion_params* p, const float* scale, void* ws,
                       size_t ws_bytes, float* red, int* dev_status,
                       void* stream);
+
+/* ------------------------------------------------------------------------
+ * Around the optimizer step: the 8-bit products, the norm and the
+ * distillation loss of the training step that feeds it gradients and reads
+ * its weights.  None of these has a counterpart on the pages: they are a
+ * service of this library.
+ *
+ * Token matrices: rows are tokens.  Unlike the batches above they may be
+ * empty (0 rows, or 0 columns where a call says so); pointers of empty
+ * matrices are not looked at.  Any row pitch and any alignment to the
+ * element size is taken; rows that start on 16-byte boundaries are faster.
+ * Sums, norms and softmax statistics are held in fp32 or wider.
+ * 8-bit matrices hold signed integers, one byte each (`ld` in bytes).
+ */
+
+/*
+ * quantize_int8 -- matrices to 8-bit integers, symmetric, to nearest even:
+ *   transpose 0:  scale_i = max_j |x_ij| / 127,  q_ij = rint(x_ij / scale_i)
+ *                 Q[i] has X[i]'s shape, scale[i] one float per row;
+ *   transpose 1:  scale_j = max_i |x_ij| / 127,  q_ji = rint(x_ij / scale_j)
+ *                 Q[i] is cols x rows (X's columns are Q's rows), scale[i]
+ *                 one float per row of Q[i].
+ * (q may differ from the exact quotient's rounding where that lies within
+ * 1e-5 of a half.)  An all-zero row gets scale 0 and zeros; a row with a NaN or
+ * an infinity gets scale NaN and zeros, so that every product with it is
+ * NaN.  scale: host array of nmat device pointers.  X: dtype x_dtype.  Use:
+ * the weights after apply_update (both orders: products with W and with its
+ * transpose), activations, gradients.
+ */
+int quantize_int8(const ouo_mat* X, int x_dtype, const ouo_mat* Q,
+                  float* const* scale, int nmat, int transpose, void* stream);
+
+/*
+ * int8_matmul -- D[i] = diag(a_scale[i]) (A[i] B[i]^T) diag(b_scale[i]):
+ * A[i] (M x K) and B[i] (N x K) 8-bit integers (-128 included), the sums
+ * exact in 32 bits, then (sum * a_scale) * b_scale in fp32, rounded once to
+ * D's type.  D[i]: M x N, dtype d_dtype.  a_scale, b_scale: host arrays of
+ * nmat device pointers, M and N floats.  K <= OUO_INT8_MAX_DEPTH; K = 0
+ * writes zeros times the scales.  M and N may be 0.  D must not overlap the
+ * operands.  With operands from quantize_int8 the three products of a linear
+ * layer Y = X W^T are
+ *   Y  = int8_matmul(q(X), q(W)),  dX = int8_matmul(q(dY), q^T(W)),
+ *   dW = int8_matmul(q^T(dY), q^T(X)),   q^T = quantize_int8 transposed,
+ * and dW is the G of dion_momentum_update.
+ */
+int int8_matmul(const ouo_mat* A, const float* const* a_scale,
+                const ouo_mat* B, const float* const* b_scale,
+                const ouo_mat* D, int d_dtype, int nmat, int* dev_status,
+                void* stream);
+
+/*
+ * rms_norm -- per row t:
+ *   h = X + residual  (rounded to H's type, written to H; X when residual
+ *                      and H are NULL),
+ *   r = 1 / sqrt(mean_j h_j^2 + eps),  y_j = h_j r weight_j.
+ * Outputs, at least one of Y and Q: Y (y rounded to y_dtype); Q and scale (y
+ * in 8 bits as quantize_int8 without transposition); rstd (optional, r per
+ * row, for the gradient).  residual and H share h_dtype; H may be the residual
+ * or X itself (same pointer, type and pitch).  Other outputs must not overlap
+ * inputs.  weight: device vector of cols elements, w_dtype.
+ *
+ * rms_norm_backward -- dY: gradient of y (through the 8-bit rounding it
+ * passes unchanged), H and rstd as above, dH: gradient that reaches h past
+ * the norm (optional, dx_dtype):
+ *   dX = dH + r (w dY - h r^2 mean_j(w_j dY_j h_j))
+ *   dweight_j = sum_t dY_tj h_tj r_t   (optional, fp32; summed in a fixed
+ *               order; needs the workspace, 16-byte aligned)
+ * dX is the gradient of X and of the residual.  dX may be dY or dH itself.
+ */
+int rms_norm(const ouo_mat* X, int x_dtype, const ouo_mat* residual,
+             const ouo_mat* H, int h_dtype, const void* weight, int w_dtype,
+             float eps, const ouo_mat* Y, int y_dtype, const ouo_mat* Q,
+             float* scale, float* rstd, void* stream);
+size_t rms_norm_backward_workspace_bytes(int64_t rows, int64_t cols);
+int rms_norm_backward(const ouo_mat* dY, int dy_dtype, const ouo_mat* H,
+                      int h_dtype, const void* weight, int w_dtype,
+                      const float* rstd, const ouo_mat* dH, const ouo_mat* dX,
+                      int dx_dtype, float* dweight, void* ws, size_t ws_bytes,
+                      void* stream);
+
+/*
+ * distill_loss -- the student's logits S (rows x V) against the teacher's
+ * top logits: row t has K entries (teacher_tk, idx_tk).  With p the softmax
+ * of teacher / tau over the row's entries and q the softmax of S / tau over
+ * the vocabulary,
+ *   loss_t = tau^2 sum_k p_k (log p_k - log q_{idx_k}),
+ *   lse_t  = log sum_v exp(S_tv / tau)          (for the gradient).
+ * Entries whose index is outside [0, V) or whose logit is -inf do not count
+ * (padding); a row without entries has loss 0 and lse 0.  An index that
+ * appears twice counts twice.  Masked student logits (-inf or the type's
+ * lowest value) have q = 0: the loss is infinite (very large) where the teacher has
+ * weight there; a row whose logits are all masked is not meaningful.
+ * idx: int32 matrix.  K <= OUO_DISTILL_MAX_ENTRIES, temperature tau in
+ * [1e-3, 1e3].  Rows may be 0.
+ *
+ * distill_loss_backward -- dloss: gradient of each row's loss (device
+ * float[rows]), lse from distill_loss:
+ *   dS_tv = dloss_t tau (q_v - sum_{k: idx_k = v} p_k)
+ * Rows with dloss 0 or without entries get zeros, whatever S holds there.
+ * dS may be S itself (same type and pitch), else they must not overlap.
+ */
+int distill_loss(const ouo_mat* S, int s_dtype, const ouo_mat* teacher,
+                 int t_dtype, const ouo_mat* idx, float temperature,
+                 float* loss, float* lse, void* stream);
+int distill_loss_backward(const ouo_mat* S, int s_dtype,
+                          const ouo_mat* teacher, int t_dtype,
+                          const ouo_mat* idx, float temperature,
+                          const float* lse, const float* dloss,
+                          const ouo_mat* dS, int ds_dtype, void* stream);
 
 #ifdef __cplusplus
 }

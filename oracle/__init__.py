@@ -32,6 +32,9 @@ Modules:
 * ``dion``      Householder QR, column normalization, the Dion / Orth-Dion step,
                 and ``effective_rank`` (a reading of Ada-Orth-Dion's estimator).
 * ``apply``     the weight update.
+* ``tokens``    8-bit quantization and product, root-mean-square norm,
+                distillation loss, with gradients (from their formulas; the
+                pages do not cover them).
 
 Every function is pinned by tests under ``tests/`` to facts fixed by the pages
 or by mathematics (closed forms through the SVD, exact rational equality,
@@ -40,6 +43,6 @@ reading taken of Ada-Orth-Dion's entropy-based rank estimator, is pinned to
 its own closed forms only.  The pages define no estimator, so its parity
 with the method is unpinned.
 """
-from . import apply, dion, dion3, momentum, ns  # noqa: F401
+from . import apply, dion, dion3, momentum, ns, tokens  # noqa: F401
 
-__all__ = ["apply", "dion", "dion3", "momentum", "ns"]
+__all__ = ["apply", "dion", "dion3", "momentum", "ns", "tokens"]

@@ -32,6 +32,8 @@ OUO_DION_QR = 1
 OUO_STATUS_TIMEOUT = 1
 OUO_STATUS_BREAKDOWN = 2
 OUO_MAX_RESTARTS = 8
+OUO_INT8_MAX_DEPTH = 131071
+OUO_DISTILL_MAX_ENTRIES = 1024
 OUO_NOALLOC_SCRATCH_BYTES = 64 * 1024 * 1024
 
 # every symbol the header declares
@@ -44,7 +46,9 @@ EXPORTED = (
     "dion_workspace_bytes", "dion_lowrank_step", "dion_workspace_bytes_ranks",
     "dion_lowrank_step_stats", "dion_effective_rank", "dion_shard_workspace_bytes",
     "dion_shard_red_floats", "dion_shard_project", "dion_shard_orth1", "dion_shard_orth2",
-    "dion_shard_update",
+    "dion_shard_update", "quantize_int8", "int8_matmul", "rms_norm",
+    "rms_norm_backward_workspace_bytes", "rms_norm_backward", "distill_loss",
+    "distill_loss_backward",
 )
 
 
@@ -120,6 +124,13 @@ _PROTOS = {
     "dion_shard_orth1": (_I, [_MP, _MP, _I, _DP, _P, _P, _SZ, _P, _P, _P]),
     "dion_shard_orth2": (_I, [_MP, _MP, _I, _DP, _P, _P, _SZ, _P, _P, _P]),
     "dion_shard_update": (_I, [_MP, _MP, _MP, _I, _I, _DP, _P, _P, _SZ, _P, _P, _P]),
+    "quantize_int8": (_I, [_MP, _I, _MP, _P, _I, _I, _P]),
+    "int8_matmul": (_I, [_MP, _P, _MP, _P, _MP, _I, _I, _P, _P]),
+    "rms_norm": (_I, [_MP, _I, _MP, _MP, _I, _P, _I, _F, _MP, _I, _MP, _P, _P, _P]),
+    "rms_norm_backward_workspace_bytes": (_SZ, [_I64, _I64]),
+    "rms_norm_backward": (_I, [_MP, _I, _MP, _I, _P, _I, _P, _MP, _MP, _I, _P, _P, _SZ, _P]),
+    "distill_loss": (_I, [_MP, _I, _MP, _I, _MP, _F, _P, _P, _P]),
+    "distill_loss_backward": (_I, [_MP, _I, _MP, _I, _MP, _F, _P, _P, _MP, _I, _P]),
 }
 
 
