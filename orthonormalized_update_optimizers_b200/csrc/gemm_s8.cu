@@ -1,6 +1,25 @@
 // int8_matmul: D = diag(a_scale) (A B^T) diag(b_scale), A (M x K) and B
 // (N x K) 8-bit integers, the products summed exactly in 32 bits.
+//
+// Tensor cores (tcgen05.mma kind::i8, 32-bit integer accumulators in TMEM),
+// operands staged by TMA, 128 bytes of K per stage in the 128-byte swizzle:
+//   * pair kernel: clusters of two CTAs share a 256 x BN tile (each stages its
+//     128 rows of A and half of B's rows); persistent, two accumulators in
+//     TMEM, so that a tile's epilogue (scales, rounding, store) runs under the
+//     next tile's products.  Bound by the tensor pipe.
+//   * split kernel: for few tokens, or outputs of few tiles.  128 rows of one
+//     operand x BN rows of the other per cluster; the cluster's CTAs split K,
+//     and join their 32-bit sums through distributed shared memory (integer
+//     sums: the same bits in any order).  Bound by reading the larger operand.
+// Matrices whose rows do not start on 16-byte boundaries cannot be read by the
+// TMA; they take a CUDA-core kernel (dp4a).
+#include <cuda.h>
+
+#include <cstring>
+#include <mutex>
+
 #include "tokens.cuh"
+#include "umma.cuh"
 
 namespace ouo {
 namespace {
@@ -56,6 +75,662 @@ s8_simt_kernel(const int8_t* A, int64_t lda, const int8_t* B, int64_t ldb, const
   }
 }
 
+
+// ------------------------------------------------------------ tensor cores
+
+constexpr uint32_t kRowB = 128;                // bytes of K per stage
+constexpr uint32_t kABytes = 128 * kRowB;      // 128 operand rows
+constexpr int kEpiWarps = 8;
+constexpr int kPairThreads = 64 + 32 * kEpiWarps;
+constexpr int kGroupM = 8;  // row tiles that share B's columns in L2
+
+struct S8Args {
+  CUtensorMap tmA, tmB, tmD;
+  const float* as;
+  const float* bs;
+  void* D;
+  int64_t ldd;
+  int bf16, tma_out;
+  int M, N, nk;          // nk: K in stages
+  int tiles_m, tiles_n;
+  int64_t total;
+  int* status;
+};
+
+// 128-byte swizzle positions of a 32 x 32 fp32 chunk, 64-byte ones of a bf16
+// chunk: what the TMA store expects, and free of bank conflicts.
+__device__ __forceinline__ int stg32(int row, int col) {
+  return row * 32 + ((((col >> 2) ^ row) & 7) << 2) + (col & 3);
+}
+__device__ __forceinline__ int stg16(int row, int col) {
+  return row * 32 + ((((col >> 3) ^ (row >> 1)) & 3) << 3) + (col & 7);
+}
+
+template <int BN>
+struct PairCfg {
+  static constexpr uint32_t kBBytes = (BN / 2) * kRowB;  // this CTA's half of B
+  static constexpr uint32_t kStage = kABytes + kBBytes;
+  static constexpr int kStages = BN == 256 ? 5 : 6;
+  static constexpr uint32_t kTmemCols = 2 * BN;
+  static constexpr uint32_t kEpi = kEpiWarps * 2 * 4096;  // two 4 KB buffers a warp
+  static constexpr size_t kSmem = 1024 + (size_t)kStages * kStage + kEpi + 512;
+};
+
+__device__ __forceinline__ void decode(const S8Args& a, int64_t t, int* ti, int* tj) {
+  const int64_t width = (int64_t)kGroupM * a.tiles_n;
+  const int g = (int)(t / width);
+  const int64_t r = t - g * width;
+  const int first = g * kGroupM;
+  const int rows = min(a.tiles_m - first, kGroupM);
+  *tj = (int)(r / rows);
+  *ti = first + (int)(r - (int64_t)*tj * rows);
+}
+
+template <int BN>
+__global__ void __launch_bounds__(kPairThreads, 1)
+s8_pair_kernel(const __grid_constant__ S8Args a) {
+  using C = PairCfg<BN>;
+  constexpr uint32_t kIdesc = ptx::instr_desc_s8(BN, 256);
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  uint8_t* epi = smem + C::kStages * C::kStage;
+  uint64_t* full = reinterpret_cast<uint64_t*>(epi + C::kEpi);
+  uint64_t* empty = full + C::kStages;
+  uint64_t* tfull = empty + C::kStages;
+  uint64_t* tempty = tfull + 2;
+  uint64_t* drain = tempty + 2;
+  uint32_t* holder = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(holder + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = ptx::cluster_ctarank();
+  const int64_t tile0 = blockIdx.x / 2, step = gridDim.x / 2;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      ptx::mbar_init(&full[s], 1);
+      ptx::mbar_init(&empty[s], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      ptx::mbar_init(&tfull[s], 1);
+      ptx::mbar_init(&tempty[s], kEpiWarps * 2);
+    }
+    ptx::mbar_init(drain, 1);
+    *abort_flag = 0;
+    ptx::fence_barrier_init();
+    ptx::prefetch_tmap(&a.tmA);
+    ptx::prefetch_tmap(&a.tmB);
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc2(holder, C::kTmemCols);
+    ptx::tmem_relinquish2();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::cluster_sync();
+  ptx::tc_fence_after();
+  const uint32_t tmem = *holder;
+
+  if (warp == 0 && lane == 0) {
+    // producer: both CTAs' loads complete on the even CTA's stage barrier
+    uint32_t stage = 0, phase = 0;
+    int64_t issued = 0;
+    bool ok = true;
+    for (int64_t t = tile0; ok && t < a.total; t += step) {
+      int ti, tj;
+      decode(a, t, &ti, &tj);
+      const int32_t arow = ti * 256 + (int32_t)rank * 128;
+      const int32_t brow = tj * BN + (int32_t)rank * (BN / 2);
+      for (int kb = 0; kb < a.nk; ++kb) {
+        if (!ptx::mbar_wait(&empty[stage], phase ^ 1, abort_flag)) {
+          ok = false;
+          break;
+        }
+        if (rank == 0) ptx::mbar_arrive_expect_tx(&full[stage], 2 * C::kStage);
+        const uint32_t fb = ptx::mapa(ptx::smem_u32(&full[stage]), 0);
+        uint8_t* sa = smem + stage * C::kStage;
+        ptx::tma_load_2d_pair(sa, &a.tmA, fb, kb * (int)kRowB, arow);
+        ptx::tma_load_2d_pair(sa + kABytes, &a.tmB, fb, kb * (int)kRowB, brow);
+        ++issued;
+        if (++stage == (uint32_t)C::kStages) { stage = 0; phase ^= 1; }
+      }
+    }
+    if (!ok) {
+      *abort_flag = 1;
+      report_status(a.status, OUO_STATUS_TIMEOUT);
+      // loads in flight land before the CTA exits: the even CTA waits for
+      // its barriers' last fill, the odd one (whose loads signal the even
+      // CTA) a fixed 2 ms, far longer than a load takes
+      if (rank != 0) {
+        const uint64_t t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < 2000000ull) {
+        }
+        issued = 0;
+      }
+      for (int s = 0; s < C::kStages; ++s) {
+        const int64_t fills = issued / C::kStages + (s < issued % C::kStages ? 1 : 0);
+        if (fills > 0)
+          ptx::mbar_wait_timed(&full[s], (uint32_t)((fills - 1) & 1), 100000000ull);
+      }
+    }
+  } else if (warp == 1 && lane == 0 && rank == 0) {
+    // MMA issuer
+    uint32_t stage = 0, phase = 0;
+    bool ok = true;
+    int64_t local = 0;
+    for (int64_t t = tile0; ok && t < a.total; t += step, ++local) {
+      const uint32_t buf = (uint32_t)(local & 1);
+      if (!ptx::mbar_wait(&tempty[buf], (uint32_t)((local >> 1) & 1) ^ 1, abort_flag)) {
+        ok = false;
+        break;
+      }
+      ptx::tc_fence_after();
+      const uint32_t d = tmem + buf * BN;
+      for (int kb = 0; kb < a.nk; ++kb) {
+        if (!ptx::mbar_wait(&full[stage], phase, abort_flag)) {
+          ok = false;
+          break;
+        }
+        ptx::tc_fence_after();
+        const uint32_t sa = ptx::smem_u32(smem + stage * C::kStage);
+#pragma unroll
+        for (uint32_t kk = 0; kk < 4; ++kk)
+          ptx::mma2_i8(d, ptx::smem_desc_sw128(sa + kk * 32, 16, 1024),
+                       ptx::smem_desc_sw128(sa + kABytes + kk * 32, 16, 1024), kIdesc,
+                       (kb > 0 || kk > 0) ? 1u : 0u);
+        ptx::mma2_commit(&empty[stage], 0x3);
+        if (++stage == (uint32_t)C::kStages) { stage = 0; phase ^= 1; }
+      }
+      if (!ok) break;
+      ptx::mma2_commit(&tfull[buf], 0x3);
+    }
+    if (!ok) {
+      *abort_flag = 1;
+      report_status(a.status, OUO_STATUS_TIMEOUT);
+    }
+    ptx::mma2_commit(drain, 0x1);
+    ptx::mbar_wait_timed(drain, 0, kWaitLimitNs);
+  } else if (warp >= 2) {
+    // epilogue: one TMEM lane quarter and half of the columns per warp
+    const uint32_t q = (uint32_t)(warp & 3), half = (uint32_t)((warp - 2) >> 2);
+    constexpr int kCh = BN / 64;  // 32-column chunks per warp
+    const uint32_t tempty_lead = ptx::mapa(ptx::smem_u32(tempty), 0);
+    float* const stg0 = reinterpret_cast<float*>(epi + (warp - 2) * 8192);
+    uint32_t nst = 0;
+    int64_t local = 0;
+    for (int64_t t = tile0; t < a.total; t += step, ++local) {
+      int ti, tj;
+      decode(a, t, &ti, &tj);
+      const uint32_t buf = (uint32_t)(local & 1);
+      const int row0 = ti * 256 + (int)rank * 128 + (int)q * 32;
+      const int col0 = tj * BN + (int)half * (BN / 2);
+      const float as = row0 + lane < a.M ? a.as[row0 + lane] : 0.f;
+      float bs[kCh];  // lane's column of each chunk
+#pragma unroll
+      for (int c = 0; c < kCh; ++c)
+        bs[c] = col0 + c * 32 + lane < a.N ? a.bs[col0 + c * 32 + lane] : 0.f;
+      int ok = 1;
+      if (lane == 0) ok = ptx::mbar_wait(&tfull[buf], (uint32_t)((local >> 1) & 1), abort_flag) ? 1 : 0;
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (!ok) {
+        if (lane == 0) {
+          *abort_flag = 1;
+          report_status(a.status, OUO_STATUS_TIMEOUT);
+        }
+        break;
+      }
+      ptx::tc_fence_after();
+#pragma unroll
+      for (int c = 0; c < kCh; ++c) {
+        const int gj0 = col0 + c * 32;
+        if (row0 >= a.M || gj0 >= a.N) continue;
+        float v[32];
+        ptx::tmem_ld32(tmem + ((q * 32u) << 16) + buf * BN + half * (BN / 2) + c * 32, v);
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          v[j] = (float)__float_as_int(v[j]) * as * __shfl_sync(0xffffffffu, bs[c], j);
+        float* stg = stg0 + (nst & 1u) * 1024;
+        if (a.tma_out) {
+          // the store before last has finished reading this buffer
+          if (lane == 0) ptx::bulk_wait_read1();
+          __syncwarp();
+          if (!a.bf16) {
+#pragma unroll
+            for (int j = 0; j < 32; j += 4)
+              *reinterpret_cast<float4*>(stg + stg32(lane, j)) =
+                  make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+          } else {
+            uint16_t* h = reinterpret_cast<uint16_t*>(stg);
+#pragma unroll
+            for (int j = 0; j < 32; j += 8)
+              *reinterpret_cast<uint4*>(h + stg16(lane, j)) =
+                  make_uint4(pack_bf16x2(v[j], v[j + 1]), pack_bf16x2(v[j + 2], v[j + 3]),
+                             pack_bf16x2(v[j + 4], v[j + 5]), pack_bf16x2(v[j + 6], v[j + 7]));
+          }
+          ptx::fence_async_shared();
+          __syncwarp();
+          if (lane == 0) {
+            ptx::tma_store_2d(&a.tmD, stg, gj0, row0);
+            ptx::bulk_commit();
+          }
+          ++nst;
+        } else {
+          __syncwarp();
+#pragma unroll
+          for (int j = 0; j < 32; j += 4)
+            *reinterpret_cast<float4*>(stg + stg32(lane, j)) =
+                make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+          __syncwarp();
+          if (gj0 + lane < a.N)
+            for (int r = 0; r < 32 && row0 + r < a.M; ++r)
+              st1(a.D, (int64_t)(row0 + r) * a.ldd + gj0 + lane, stg[stg32(r, lane)], a.bf16);
+        }
+      }
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive_cluster(tempty_lead + buf * 8u);
+    }
+    if (lane == 0) ptx::bulk_wait0();
+    __syncwarp();
+  }
+  __syncthreads();
+  ptx::cluster_sync();
+  if (warp == 1) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc2(tmem, C::kTmemCols);
+  }
+}
+
+// ------------------------------------------------------------ split kernel
+
+constexpr int kSplitThreads = 192;
+
+struct SplitArgs {
+  CUtensorMap tmR, tmT;  // R: 128 rows a tile; T: BN rows a tile
+  const float* rs;
+  const float* ts;
+  void* D;
+  int64_t ldd;
+  int bf16;
+  int t_rows;   // D's rows are T's rows (else R's)
+  int R, T, nk, nk_cta;
+  int tiles_t;
+  int vec;      // D rows allow 4-element stores
+  int* status;
+};
+
+template <int BN>
+struct SplitCfg {
+  static constexpr uint32_t kTBytes = BN * kRowB;
+  static constexpr uint32_t kStage = kABytes + kTBytes;
+  static constexpr int kStages = 4;
+  static constexpr uint32_t kTmemCols = BN < 32 ? 32 : BN;
+  static constexpr size_t kSmem = 1024 + (size_t)kStages * kStage + 256;
+  static_assert((size_t)BN * 512 <= (size_t)kStages * kStage, "partial sums reuse the stages");
+};
+
+template <int BN>
+__global__ void __launch_bounds__(kSplitThreads)
+s8_split_kernel(const __grid_constant__ SplitArgs a) {
+  using C = SplitCfg<BN>;
+  constexpr uint32_t kIdesc = ptx::instr_desc_s8(BN);
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kStages * C::kStage);
+  uint64_t* empty = full + C::kStages;
+  uint64_t* done = empty + C::kStages;
+  uint32_t* holder = reinterpret_cast<uint32_t*>(done + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(holder + 1);
+  int* part = reinterpret_cast<int*>(smem);  // [BN][128], after the products
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint32_t rank = ptx::cluster_ctarank(), nsplit;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(nsplit));
+  const int tile = (int)(blockIdx.x / nsplit);
+  const int r0 = tile / a.tiles_t * 128, t0 = tile % a.tiles_t * BN;
+  const int kb0 = (int)rank * a.nk_cta, kb1 = min(a.nk, kb0 + a.nk_cta);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      ptx::mbar_init(&full[s], 1);
+      ptx::mbar_init(&empty[s], 1);
+    }
+    ptx::mbar_init(done, 1);
+    *abort_flag = 0;
+    ptx::fence_barrier_init();
+    ptx::prefetch_tmap(&a.tmR);
+    ptx::prefetch_tmap(&a.tmT);
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc(holder, C::kTmemCols);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = *holder;
+
+  if (warp == 0 && lane == 0) {
+    uint32_t stage = 0, phase = 0;
+    int issued = 0;
+    bool ok = true;
+    for (int kb = kb0; kb < kb1; ++kb) {
+      if (!ptx::mbar_wait(&empty[stage], phase ^ 1, abort_flag)) {
+        ok = false;
+        break;
+      }
+      ptx::mbar_arrive_expect_tx(&full[stage], C::kStage);
+      uint8_t* s = smem + stage * C::kStage;
+      ptx::tma_load_2d(s, &a.tmR, &full[stage], kb * (int)kRowB, r0);
+      ptx::tma_load_2d(s + kABytes, &a.tmT, &full[stage], kb * (int)kRowB, t0);
+      ++issued;
+      if (++stage == (uint32_t)C::kStages) { stage = 0; phase ^= 1; }
+    }
+    if (!ok) {
+      *abort_flag = 1;
+      report_status(a.status, OUO_STATUS_TIMEOUT);
+      for (int s = 0; s < C::kStages; ++s) {
+        const int fills = issued / C::kStages + (s < issued % C::kStages ? 1 : 0);
+        if (fills > 0)
+          ptx::mbar_wait_timed(&full[s], (uint32_t)((fills - 1) & 1), 100000000ull);
+      }
+    }
+  } else if (warp == 1 && lane == 0) {
+    uint32_t stage = 0, phase = 0;
+    for (int kb = kb0; kb < kb1; ++kb) {
+      if (!ptx::mbar_wait(&full[stage], phase, abort_flag)) {
+        *abort_flag = 1;
+        report_status(a.status, OUO_STATUS_TIMEOUT);
+        break;
+      }
+      ptx::tc_fence_after();
+      const uint32_t s = ptx::smem_u32(smem + stage * C::kStage);
+#pragma unroll
+      for (uint32_t kk = 0; kk < 4; ++kk)
+        ptx::mma_i8(tmem, ptx::smem_desc_sw128(s + kk * 32, 16, 1024),
+                    ptx::smem_desc_sw128(s + kABytes + kk * 32, 16, 1024), kIdesc,
+                    (kb > kb0 || kk > 0) ? 1u : 0u);
+      ptx::mma_commit(&empty[stage]);
+      if (++stage == (uint32_t)C::kStages) { stage = 0; phase ^= 1; }
+    }
+    ptx::mma_commit(done);
+    // after an aborted loop too: TMEM is released only when this is over
+    ptx::mbar_wait_timed(done, 0, kWaitLimitNs);
+  }
+  __syncwarp();
+  __syncthreads();  // the products are done, the stages are free
+  const uint32_t q = (uint32_t)(warp & 3);
+  if (warp >= 2) {
+    ptx::tc_fence_after();
+    constexpr int kStep = BN < 32 ? 16 : 32;
+#pragma unroll 1
+    for (int c = 0; c < BN; c += kStep) {
+      float v[kStep];
+      if (kb1 > kb0) {
+        if (kStep == 16) ptx::tmem_ld16(tmem + ((q * 32u) << 16) + c, v);
+        else ptx::tmem_ld32(tmem + ((q * 32u) << 16) + c, v);
+      } else {
+#pragma unroll
+        for (int j = 0; j < kStep; ++j) v[j] = 0.f;
+      }
+#pragma unroll
+      for (int j = 0; j < kStep; ++j)
+        part[(c + j) * 128 + q * 32 + lane] = __float_as_int(v[j]);
+    }
+    ptx::tc_fence_before();
+  }
+  __syncwarp();
+  ptx::cluster_sync();
+  // The CTAs of a cluster divide the T rows of the tile: CTA `rank` sums and
+  // writes rows rank, rank + nsplit, ...
+  if (warp >= 2) {
+    const uint32_t base = ptx::smem_u32(part);
+    if (a.t_rows) {
+      const int r = r0 + 4 * lane;
+      float rs[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) rs[i] = r + i < a.R ? a.rs[r + i] : 0.f;
+      for (int j = (int)rank + (int)nsplit * (warp - 2); j < BN && t0 + j < a.T;
+           j += 4 * (int)nsplit) {
+        int4 s = make_int4(0, 0, 0, 0);
+        for (uint32_t p = 0; p < nsplit; ++p) {
+          const int4 x = ptx::ld_cluster_int4(
+              ptx::mapa(base + (uint32_t)(j * 128 + 4 * lane) * 4u, p));
+          s.x += x.x; s.y += x.y; s.z += x.z; s.w += x.w;
+        }
+        const float ts = a.ts[t0 + j];
+        // (sum * a_scale) * b_scale: T is A here
+        const float v[4] = {(float)s.x * ts * rs[0], (float)s.y * ts * rs[1],
+                            (float)s.z * ts * rs[2], (float)s.w * ts * rs[3]};
+        const int64_t o = (int64_t)(t0 + j) * a.ldd + r;
+        if (a.vec && r + 3 < a.R) {
+          if (a.bf16)
+            *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.D) + o) =
+                make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+          else
+            *reinterpret_cast<float4*>(reinterpret_cast<float*>(a.D) + o) =
+                make_float4(v[0], v[1], v[2], v[3]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (r + i < a.R) st1(a.D, o + i, v[i], a.bf16);
+        }
+      }
+    } else {
+      const int row = (warp - 2) * 32 + lane;
+      const float rs = r0 + row < a.R ? a.rs[r0 + row] : 0.f;
+      const int per = (BN + (int)nsplit - 1) / (int)nsplit;
+      for (int j = (int)rank * per; j < BN && j < ((int)rank + 1) * per && t0 + j < a.T; ++j) {
+        int s = 0;
+        for (uint32_t p = 0; p < nsplit; ++p)
+          s += ptx::ld_cluster_int(ptx::mapa(base + (uint32_t)(j * 128 + row) * 4u, p));
+        if (r0 + row < a.R)
+          st1(a.D, (int64_t)(r0 + row) * a.ldd + t0 + j, (float)s * rs * a.ts[t0 + j], a.bf16);
+      }
+    }
+  }
+  __syncwarp();
+  ptx::cluster_sync();  // peers have read this CTA's sums
+  if (warp == 1) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, C::kTmemCols);
+  }
+}
+
+// ------------------------------------------------------------------- host
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+  static EncodeTiledFn fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                         &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<EncodeTiledFn>(p);
+  });
+  return fn;
+}
+
+int make_map(CUtensorMap* map, const ouo_mat& m, CUtensorMapDataType type, size_t es,
+             uint32_t box_cols, uint32_t box_rows, CUtensorMapSwizzle swz) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return set_error(OUO_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
+  cuuint64_t dims[2] = {(cuuint64_t)m.cols, (cuuint64_t)m.rows};
+  // the pitch of a single row is not used, but has to be a valid one
+  cuuint64_t strides[1] = {m.rows > 1 ? (cuuint64_t)m.ld * es
+                                      : (cuuint64_t)align_up((size_t)m.cols * es, 16)};
+  cuuint32_t box[2] = {box_cols, box_rows};
+  cuuint32_t estr[2] = {1, 1};
+  const CUresult r = fn(map, type, 2, m.ptr, dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, swz, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return set_error(OUO_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
+  return OUO_OK;
+}
+
+int map_s8(CUtensorMap* map, const ouo_mat& m, uint32_t box_rows) {
+  return make_map(map, m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, kRowB, box_rows,
+                  CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+cudaLaunchConfig_t config(unsigned grid, unsigned threads, size_t smem, cudaStream_t s,
+                          unsigned cluster, cudaLaunchAttribute* attr) {
+  cudaLaunchConfig_t cfg;
+  memset(&cfg, 0, sizeof(cfg));
+  cfg.gridDim = dim3(grid, 1, 1);
+  cfg.blockDim = dim3(threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cluster;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cfg;
+}
+
+// What a kernel needs set once per device.
+struct Setup {
+  std::mutex mu;
+  int slots[64] = {0};  // 0: not yet set up; else resident clusters
+};
+
+template <class K>
+int setup(Setup& st, K kern, unsigned threads, size_t smem, unsigned cluster, int* slots) {
+  int dev = 0;
+  OUO_CHECK_CUDA(cudaGetDevice(&dev));
+  if (dev < 0 || dev >= 64)
+    return set_error(OUO_ERR_UNSUPPORTED, "device ordinal %d out of range", dev);
+  std::lock_guard<std::mutex> lock(st.mu);
+  if (!st.slots[dev]) {
+    OUO_CHECK_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        (int)smem));
+    int n = 0;
+    cudaLaunchAttribute attr[1];
+    cudaLaunchConfig_t cfg = config(cluster * (unsigned)num_sms(), threads, smem, nullptr, cluster, attr);
+    OUO_CHECK_CUDA(cudaOccupancyMaxActiveClusters(&n, kern, &cfg));
+    if (n < 1) return set_error(OUO_ERR_UNSUPPORTED, "no cluster of the 8-bit product fits");
+    st.slots[dev] = n;
+  }
+  *slots = st.slots[dev];
+  return OUO_OK;
+}
+
+struct Product {
+  ouo_mat A, B, D;
+  const float* as;
+  const float* bs;
+  int bf16;
+  int* status;
+};
+
+template <int BN>
+int run_pair(const Product& p, cudaStream_t s) {
+  using C = PairCfg<BN>;
+  static Setup st;
+  int slots = 0;
+  OUO_TRY(setup(st, s8_pair_kernel<BN>, kPairThreads, C::kSmem, 2, &slots));
+  S8Args a;
+  memset(&a, 0, sizeof(a));
+  OUO_TRY(map_s8(&a.tmA, p.A, 128));
+  OUO_TRY(map_s8(&a.tmB, p.B, BN / 2));
+  const size_t es = p.bf16 ? 2 : 4;
+  a.tma_out = rows16(p.D, es) ? 1 : 0;
+  if (a.tma_out)
+    OUO_TRY(make_map(&a.tmD, p.D,
+                     p.bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
+                     es, 32, 32, p.bf16 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B));
+  a.as = p.as; a.bs = p.bs;
+  a.D = p.D.ptr; a.ldd = p.D.ld; a.bf16 = p.bf16;
+  a.M = (int)p.D.rows; a.N = (int)p.D.cols;
+  a.nk = (int)ceil_div(p.A.cols, (int64_t)kRowB);
+  a.tiles_m = (int)ceil_div(p.D.rows, 256);
+  a.tiles_n = (int)ceil_div(p.D.cols, BN);
+  a.total = (int64_t)a.tiles_m * a.tiles_n;
+  a.status = p.status;
+  const int64_t n = a.total < slots ? a.total : slots;
+  cudaLaunchAttribute attr[1];
+  cudaLaunchConfig_t cfg = config((unsigned)(2 * n), kPairThreads, C::kSmem, s, 2, attr);
+  OUO_CHECK_CUDA(cudaLaunchKernelEx(&cfg, s8_pair_kernel<BN>, a));
+  OUO_CHECK_LAUNCH();
+  return OUO_OK;
+}
+
+// t_rows: T is A (D's rows), R is B; else the other way round.
+template <int BN>
+int run_split(const Product& p, bool t_rows, unsigned nsplit, cudaStream_t s) {
+  using C = SplitCfg<BN>;
+  static Setup st;
+  int slots = 0;
+  OUO_TRY(setup(st, s8_split_kernel<BN>, kSplitThreads, C::kSmem, 1, &slots));
+  SplitArgs a;
+  memset(&a, 0, sizeof(a));
+  const ouo_mat& R = t_rows ? p.B : p.A;
+  const ouo_mat& T = t_rows ? p.A : p.B;
+  OUO_TRY(map_s8(&a.tmR, R, 128));
+  OUO_TRY(map_s8(&a.tmT, T, BN));
+  a.rs = t_rows ? p.bs : p.as;
+  a.ts = t_rows ? p.as : p.bs;
+  a.D = p.D.ptr; a.ldd = p.D.ld; a.bf16 = p.bf16;
+  a.t_rows = t_rows ? 1 : 0;
+  a.R = (int)R.rows; a.T = (int)T.rows;
+  a.nk = (int)ceil_div(R.cols, (int64_t)kRowB);
+  a.nk_cta = (int)ceil_div(a.nk, (int64_t)nsplit);
+  a.tiles_t = (int)ceil_div(T.rows, BN);
+  const size_t es4 = p.bf16 ? 8 : 16;
+  a.vec = (uintptr_t)p.D.ptr % es4 == 0 && (p.D.rows <= 1 || p.D.ld % 4 == 0);
+  a.status = p.status;
+  const int64_t tiles = ceil_div(R.rows, 128) * (int64_t)a.tiles_t;
+  if (tiles * nsplit > 0x7fffffff) return set_error(OUO_ERR_UNSUPPORTED, "D: too many tiles");
+  cudaLaunchAttribute attr[1];
+  cudaLaunchConfig_t cfg = config((unsigned)(tiles * nsplit), kSplitThreads, C::kSmem, s, nsplit, attr);
+  OUO_CHECK_CUDA(cudaLaunchKernelEx(&cfg, s8_split_kernel<BN>, a));
+  OUO_CHECK_LAUNCH();
+  return OUO_OK;
+}
+
+int run_simt(const Product& p, cudaStream_t s) {
+  const int64_t tn = ceil_div(p.D.cols, 64), tiles = ceil_div(p.D.rows, 64) * tn;
+  if (tiles > 0x7fffffff) return set_error(OUO_ERR_UNSUPPORTED, "D: too many tiles");
+  s8_simt_kernel<<<(unsigned)tiles, 256, 0, s>>>(
+      (const int8_t*)p.A.ptr, p.A.ld, (const int8_t*)p.B.ptr, p.B.ld, p.as, p.bs, p.D.ptr, p.D.ld,
+      p.bf16, p.D.rows, p.D.cols, p.A.cols, tn);
+  OUO_CHECK_LAUNCH();
+  return OUO_OK;
+}
+
+int product(const Product& p, cudaStream_t s) {
+  const int64_t M = p.D.rows, N = p.D.cols, K = p.A.cols;
+  if (M == 0 || N == 0) return OUO_OK;
+  if (K == 0 || !rows16(p.A, 1) || !rows16(p.B, 1)) return run_simt(p, s);
+  const int64_t pairs = num_sms() / 2;
+  const int64_t tiles = ceil_div(M, 256) * ceil_div(N, 256);
+  if (M > 128 && N > 128 && tiles >= pairs) return run_pair<256>(p, s);
+  // T is the side with fewer rows, A unless B's rows are few
+  const bool t_rows = M <= N || N > 128;
+  const int64_t T = t_rows ? M : N, R = t_rows ? N : M;
+  const int bn = T <= 16 ? 16 : T <= 32 ? 32 : T <= 64 ? 64 : 128;
+  const int64_t st = ceil_div(R, 128) * ceil_div(T, bn), nk = ceil_div(K, (int64_t)kRowB);
+  unsigned split = 1;
+  while (split < 8 && st * split < 2 * num_sms() && nk / (2 * split) >= 2) split *= 2;
+  switch (bn) {
+    case 16: return run_split<16>(p, t_rows, split, s);
+    case 32: return run_split<32>(p, t_rows, split, s);
+    case 64: return run_split<64>(p, t_rows, split, s);
+    default: return run_split<128>(p, t_rows, split, s);
+  }
+}
+
 }  // namespace
 }  // namespace ouo
 
@@ -90,13 +765,8 @@ extern "C" int int8_matmul(const ouo_mat* A, const float* const* a_scale, const 
   OUO_TRY(require_sm100());
   cudaStream_t s = (cudaStream_t)stream;
   for (int i = 0; i < nmat; ++i) {
-    if (D[i].rows == 0 || D[i].cols == 0) continue;
-    const int64_t tn = ceil_div(D[i].cols, 64), tiles = ceil_div(D[i].rows, 64) * tn;
-    if (tiles > 0x7fffffff) return set_error(OUO_ERR_UNSUPPORTED, "D[%d]: too many tiles", i);
-    s8_simt_kernel<<<(unsigned)tiles, 256, 0, s>>>(
-        (const int8_t*)A[i].ptr, A[i].ld, (const int8_t*)B[i].ptr, B[i].ld, a_scale[i], b_scale[i],
-        D[i].ptr, D[i].ld, d_dtype == OUO_BF16, D[i].rows, D[i].cols, A[i].cols, tn);
-    OUO_CHECK_LAUNCH();
+    OUO_TRY(product(Product{A[i], B[i], D[i], a_scale[i], b_scale[i], d_dtype == OUO_BF16,
+                            dev_status}, s));
   }
   return OUO_OK;
 }
