@@ -124,13 +124,14 @@ _PROTOS = {
     "dion_shard_orth1": (_I, [_MP, _MP, _I, _DP, _P, _P, _SZ, _P, _P, _P]),
     "dion_shard_orth2": (_I, [_MP, _MP, _I, _DP, _P, _P, _SZ, _P, _P, _P]),
     "dion_shard_update": (_I, [_MP, _MP, _MP, _I, _I, _DP, _P, _P, _SZ, _P, _P, _P]),
-    "quantize_int8": (_I, [_MP, _I, _MP, _P, _I, _I, _P]),
-    "int8_matmul": (_I, [_MP, _P, _MP, _P, _MP, _I, _I, _P, _P]),
-    "rms_norm": (_I, [_MP, _I, _MP, _MP, _I, _P, _I, _F, _MP, _I, _MP, _P, _P, _P]),
+    # matrices of these are packed bytes (tokens.py)
+    "quantize_int8": (_I, [_P, _I, _P, _P, _I, _I, _P]),
+    "int8_matmul": (_I, [_P, _P, _P, _P, _P, _I, _I, _P, _P]),
+    "rms_norm": (_I, [_P, _I, _P, _P, _I, _P, _I, _F, _P, _I, _P, _P, _P, _P]),
     "rms_norm_backward_workspace_bytes": (_SZ, [_I64, _I64]),
-    "rms_norm_backward": (_I, [_MP, _I, _MP, _I, _P, _I, _P, _MP, _MP, _I, _P, _P, _SZ, _P]),
-    "distill_loss": (_I, [_MP, _I, _MP, _I, _MP, _F, _P, _P, _P]),
-    "distill_loss_backward": (_I, [_MP, _I, _MP, _I, _MP, _F, _P, _P, _MP, _I, _P]),
+    "rms_norm_backward": (_I, [_P, _I, _P, _I, _P, _I, _P, _P, _P, _I, _P, _P, _SZ, _P]),
+    "distill_loss": (_I, [_P, _I, _P, _I, _P, _F, _P, _P, _P]),
+    "distill_loss_backward": (_I, [_P, _I, _P, _I, _P, _F, _P, _P, _P, _I, _P]),
 }
 
 

@@ -44,11 +44,13 @@ int num_sms() {
 }
 
 int require_sm100() {
+  static std::atomic<int> known[64];  // 1: an sm_100 part (zero-initialized)
   int dev = -1;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess)
     return set_error(OUO_ERR_NO_DEVICE, "no CUDA device: %s",
                      cudaGetErrorString(e));
+  if (dev >= 0 && dev < 64 && known[dev].load(std::memory_order_relaxed)) return OUO_OK;
   int major = 0, minor = 0;
   cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
   cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
@@ -56,6 +58,7 @@ int require_sm100() {
     return set_error(OUO_ERR_NO_DEVICE,
                      "device %d is sm_%d%d; this library is built for sm_100a",
                      dev, major, minor);
+  if (dev >= 0 && dev < 64) known[dev].store(1, std::memory_order_relaxed);
   return OUO_OK;
 }
 

@@ -11,11 +11,13 @@ asynchronous on the current stream of the tensors' device (or ``stream=``).
 from __future__ import annotations
 
 import ctypes
+import struct
 from typing import Optional, Sequence, Union
 
 import torch
 
 from . import _lib as L
+from .binding import MatBatch
 
 __all__ = [
     "int8_empty", "quantize_int8", "int8_matmul", "rms_norm", "rms_norm_backward",
@@ -26,96 +28,105 @@ Tensors = Union[torch.Tensor, Sequence[torch.Tensor]]
 
 _CODES = {torch.float32: L.OUO_F32, torch.bfloat16: L.OUO_BF16}
 
+# One ouo_mat as bytes; a batch is their concatenation.  A call's descriptors
+# live for the duration of the call.
+_mat_bytes = struct.Struct("Pqqq").pack
+_ptr_bytes = struct.Struct("P").pack
+assert struct.calcsize("Pqqq") == ctypes.sizeof(L.OuoMat)
 
-class _Call:
-    """The device and stream of one call: every tensor has to be on the
-    first one's device."""
+# The raw handle of a device's current stream: these calls take microseconds,
+# and building a Stream object is one of them.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
-    __slots__ = ("dev",)
 
-    def __init__(self):
-        self.dev = -1
+def _wrong_device(t: torch.Tensor, name: str, dev: int):
+    if not t.is_cuda:
+        return ValueError(f"{name} must be a CUDA tensor")
+    return ValueError(f"{name} is on {t.device}, the others on cuda:{dev}")
 
-    def on(self, t: torch.Tensor, name: str) -> None:
-        if not t.is_cuda:
-            raise ValueError(f"{name} must be a CUDA tensor")
-        d = t.get_device()
-        if self.dev < 0:
-            self.dev = d
-        elif d != self.dev:
-            raise ValueError(f"{name} is on cuda:{d}, the others on cuda:{self.dev}")
 
-    def mat(self, t: torch.Tensor, name: str, dtype: Optional[torch.dtype] = None) -> L.OuoMat:
-        if dtype is None:
-            if t.dtype not in _CODES:
-                raise TypeError(f"{name}: unsupported dtype {t.dtype} (float32 or bfloat16)")
-        elif t.dtype != dtype:
-            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-        if t.dim() != 2:
-            raise ValueError(f"{name} must be 2-D")
-        r, c = t.shape
-        ld, one = t.stride()
-        if c > 1 and one != 1:
-            raise ValueError(f"{name} needs unit column stride")
-        if ld < c:
-            if r > 1 and c > 0:
-                raise ValueError(f"{name}: rows overlap (stride {ld}, {c} columns)")
-            ld = c
-        self.on(t, name)
-        return L.OuoMat(t.data_ptr(), r, c, ld)
+def _code(t: torch.Tensor, name: str) -> int:
+    code = _CODES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name}: unsupported dtype {t.dtype} (float32 or bfloat16)")
+    return code
 
-    def vec(self, t: torch.Tensor, name: str, n: int,
-            dtype: Optional[torch.dtype] = torch.float32) -> int:
-        if dtype is None:
-            if t.dtype not in _CODES:
-                raise TypeError(f"{name}: unsupported dtype {t.dtype} (float32 or bfloat16)")
-        elif t.dtype != dtype:
-            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-        if t.numel() < n:
-            raise ValueError(f"{name} needs at least {n} elements, got {t.numel()}")
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-        self.on(t, name)
-        return t.data_ptr()
 
-    def run(self, fname: str, stream, *args) -> None:
-        """Calls the library with this device current and the stream last."""
-        if stream is None:
-            s = torch.cuda.current_stream(self.dev)
-        else:
-            s = stream
-            if s.device.index != self.dev:
-                raise ValueError(f"the stream is on {s.device}, the tensors on cuda:{self.dev}")
-        fn = getattr(L.lib(), fname)
-        if torch.cuda.current_device() == self.dev:
-            rc = fn(*args, s.cuda_stream)
-        else:
-            with torch.cuda.device(self.dev):
-                rc = fn(*args, s.cuda_stream)
-        if rc:
-            L.check(fname, rc)
+def _mat(t: torch.Tensor, name: str, dev: int, dtype: Optional[torch.dtype] = None) -> bytes:
+    """A 2-D row-major tensor as an ouo_mat (its dtype as `dtype` says, or
+    already looked up by _code)."""
+    if dtype is not None and t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D")
+    r, c = t.shape
+    ld, one = t.stride()
+    if one != 1 and c > 1:
+        raise ValueError(f"{name} needs unit column stride")
+    if ld < c:
+        if r > 1:
+            raise ValueError(f"{name}: rows overlap (stride {ld}, {c} columns)")
+        ld = c
+    if dev < 0 or t.get_device() != dev:
+        raise _wrong_device(t, name, dev)
+    return _mat_bytes(t.data_ptr(), r, c, ld)
+
+
+def _vec(t: torch.Tensor, name: str, dev: int, n: int,
+         dtype: Optional[torch.dtype] = torch.float32) -> int:
+    """The address of a contiguous vector of at least n elements."""
+    if dtype is not None and t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.numel() < n:
+        raise ValueError(f"{name} needs at least {n} elements, got {t.numel()}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.get_device() != dev:
+        raise _wrong_device(t, name, dev)
+    return t.data_ptr()
+
+
+def _mats(ts, name: str, dev: int, dtype: Optional[torch.dtype] = None) -> bytes:
+    if len(ts) == 1:
+        return _mat(ts[0], name, dev, dtype)
+    for t in ts:
+        if t.dtype is not ts[0].dtype:
+            raise TypeError(f"{name}: a batch must have one dtype")
+    return b"".join([_mat(t, name, dev, dtype) for t in ts])
+
+
+def _vecs(x: Tensors, name: str, dev: int, owners) -> bytes:
+    """Pointers of one fp32 vector per matrix, one element per row."""
+    ts = _list(x)
+    if len(ts) != len(owners):
+        raise ValueError(f"{name} needs one vector per matrix")
+    return b"".join([_ptr_bytes(_vec(t, name, dev, m.shape[0])) for t, m in zip(ts, owners)])
+
+
+def _run(fname: str, dev: int, stream, *args) -> None:
+    """Calls the library with the tensors' device current (the first one's,
+    which every other was compared with), the stream last."""
+    if stream is None:
+        s = _raw_stream(dev)
+    else:
+        if stream.device.index != dev:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{dev}")
+        s = stream.cuda_stream
+    fn = getattr(L.lib(), fname)
+    if torch.cuda.current_device() == dev:
+        rc = fn(*args, s)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, s)
+    if rc:
+        L.check(fname, rc)
 
 
 def _list(x: Tensors) -> Sequence[torch.Tensor]:
-    return (x,) if isinstance(x, torch.Tensor) else x
-
-
-def _mats(call: _Call, ts, name: str, dtype=None):
-    arr = (L.OuoMat * max(len(ts), 1))()
-    for i, t in enumerate(ts):
-        arr[i] = call.mat(t, name, dtype)
-        if t.dtype != ts[0].dtype:
-            raise TypeError(f"{name}: a batch must have one dtype")
-    return arr
-
-
-def _vecs(call: _Call, ts, name: str, counts):
-    if len(ts) != len(counts):
-        raise ValueError(f"{name} needs one vector per matrix")
-    arr = (ctypes.c_void_p * max(len(ts), 1))()
-    for i, t in enumerate(ts):
-        arr[i] = call.vec(t, name, counts[i])
-    return arr
+    if isinstance(x, torch.Tensor):
+        return (x,)
+    return x.tensors if isinstance(x, MatBatch) else x
 
 
 def int8_empty(rows: int, cols: int, device=None) -> torch.Tensor:
@@ -132,16 +143,16 @@ def quantize_int8(X: Tensors, Q: Tensors, scale: Tensors, transpose: bool = Fals
     """Q, scale <- X in 8 bits with one scale per row, or, with ``transpose``,
     X's transpose (one scale per column of X).  X, Q and scale are tensors, or
     lists of equal length."""
-    xs, qs, ss = _list(X), _list(Q), _list(scale)
+    xs, qs = _list(X), _list(Q)
     n = len(xs)
     if len(qs) != n:
         raise ValueError(f"X has {n} matrices, Q {len(qs)}")
     if n == 0:
         return
-    c = _Call()
-    xa, qa = _mats(c, xs, "X"), _mats(c, qs, "Q", torch.int8)
-    sa = _vecs(c, ss, "scale", [q.shape[0] for q in qs])
-    c.run("quantize_int8", stream, xa, _CODES[xs[0].dtype], qa, sa, n, 1 if transpose else 0)
+    dev, code = xs[0].get_device(), _code(xs[0], "X")
+    _run("quantize_int8", dev, stream, _mats(xs, "X", dev), code,
+         _mats(qs, "Q", dev, torch.int8), _vecs(scale, "scale", dev, qs), n,
+         1 if transpose else 0)
 
 
 def int8_matmul(A: Tensors, a_scale: Tensors, B: Tensors, b_scale: Tensors, D: Tensors,
@@ -155,17 +166,11 @@ def int8_matmul(A: Tensors, a_scale: Tensors, B: Tensors, b_scale: Tensors, D: T
         raise ValueError(f"A has {n} matrices, B {len(Bs)}, D {len(Ds)}")
     if n == 0:
         return
-    c = _Call()
-    aa, ba = _mats(c, As, "A", torch.int8), _mats(c, Bs, "B", torch.int8)
-    da = _mats(c, Ds, "D")
-    sa = _vecs(c, _list(a_scale), "a_scale", [t.shape[0] for t in As])
-    sb = _vecs(c, _list(b_scale), "b_scale", [t.shape[0] for t in Bs])
-    st = None if status is None else c.vec(status, "status", 1, torch.int32)
-    c.run("int8_matmul", stream, aa, sa, ba, sb, da, _CODES[Ds[0].dtype], n, st)
-
-
-def _ref(m: Optional[L.OuoMat]):
-    return None if m is None else ctypes.byref(m)
+    dev = As[0].get_device()
+    a, b = _mats(As, "A", dev, torch.int8), _mats(Bs, "B", dev, torch.int8)
+    st = None if status is None else _vec(status, "status", dev, 1, torch.int32)
+    _run("int8_matmul", dev, stream, a, _vecs(a_scale, "a_scale", dev, As), b,
+         _vecs(b_scale, "b_scale", dev, Bs), _mats(Ds, "D", dev), _code(Ds[0], "D"), n, st)
 
 
 def rms_norm(X: torch.Tensor, weight: torch.Tensor, Y: Optional[torch.Tensor] = None,
@@ -174,31 +179,33 @@ def rms_norm(X: torch.Tensor, weight: torch.Tensor, Y: Optional[torch.Tensor] = 
              rstd: Optional[torch.Tensor] = None, eps: float = 1e-6, stream=None) -> None:
     """H <- X + residual; Y and / or (Q, scale in 8 bits) <- the norm of H
     times weight; rstd <- 1 / sqrt(mean(H^2) + eps) per row."""
-    c = _Call()
-    x = c.mat(X, "X")
+    dev = X.get_device()
+    x = _mat(X, "X", dev)
     rows, cols = X.shape
-    w = c.vec(weight, "weight", cols, None)
-    if weight.numel() != cols:
-        raise ValueError(f"weight has {weight.numel()} elements, X {cols} columns")
     r = h = y = q = sp = rp = None
-    if residual is not None:
-        r = c.mat(residual, "residual")
-        if H is not None and H.dtype != residual.dtype:
-            raise TypeError("residual and H must have one dtype")
+    hc = yc = L.OUO_F32
     if H is not None:
-        h = c.mat(H, "H")
+        h, hc = _mat(H, "H", dev), _code(H, "H")
+    if residual is not None:
+        if H is not None and H.dtype is not residual.dtype:
+            raise TypeError("residual and H must have one dtype")
+        r = _mat(residual, "residual", dev)
     if Y is not None:
-        y = c.mat(Y, "Y")
+        y, yc = _mat(Y, "Y", dev), _code(Y, "Y")
     if Q is not None:
-        q = c.mat(Q, "Q", torch.int8)
         if scale is None:
             raise ValueError("Q needs scale")
-        sp = c.vec(scale, "scale", rows)
+        q, sp = _mat(Q, "Q", dev, torch.int8), _vec(scale, "scale", dev, rows)
     if rstd is not None:
-        rp = c.vec(rstd, "rstd", rows)
-    c.run("rms_norm", stream, ctypes.byref(x), _CODES[X.dtype], _ref(r), _ref(h),
-          L.OUO_F32 if H is None else _CODES[H.dtype], w, _CODES[weight.dtype], eps, _ref(y),
-          L.OUO_F32 if Y is None else _CODES[Y.dtype], _ref(q), sp, rp)
+        rp = _vec(rstd, "rstd", dev, rows)
+    _run("rms_norm", dev, stream, x, _code(X, "X"), r, h, hc, _weight(weight, dev, cols),
+         _code(weight, "weight"), eps, y, yc, q, sp, rp)
+
+
+def _weight(weight: torch.Tensor, dev: int, cols: int) -> int:
+    if weight.numel() != cols:
+        raise ValueError(f"weight has {weight.numel()} elements, the rows {cols}")
+    return _vec(weight, "weight", dev, cols, None)
 
 
 def rms_norm_backward_workspace_bytes(rows: int, cols: int) -> int:
@@ -212,57 +219,46 @@ def rms_norm_backward(dY: torch.Tensor, H: torch.Tensor, weight: torch.Tensor,
                       workspace: Optional[torch.Tensor] = None, stream=None) -> None:
     """dX <- dH + the gradient of rms_norm's H; dweight <- that of its
     weight."""
-    c = _Call()
-    dy, h, dx = c.mat(dY, "dY"), c.mat(H, "H"), c.mat(dX, "dX")
+    dev = dY.get_device()
+    dy, h, dx = _mat(dY, "dY", dev), _mat(H, "H", dev), _mat(dX, "dX", dev)
     rows, cols = dY.shape
-    w = c.vec(weight, "weight", cols, None)
-    if weight.numel() != cols:
-        raise ValueError(f"weight has {weight.numel()} elements, dY {cols} columns")
-    rp = c.vec(rstd, "rstd", rows)
+    w, rp = _weight(weight, dev, cols), _vec(rstd, "rstd", dev, rows)
     dh = dwp = wp = None
     wn = 0
     if dH is not None:
-        if dH.dtype != dX.dtype:
+        if dH.dtype is not dX.dtype:
             raise TypeError("dH and dX must have one dtype")
-        dh = c.mat(dH, "dH")
+        dh = _mat(dH, "dH", dev)
     if dweight is not None:
-        dwp = c.vec(dweight, "dweight", cols)
+        dwp = _vec(dweight, "dweight", dev, cols)
         need = rms_norm_backward_workspace_bytes(rows, cols)
         if workspace is None:
             workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dY.device)
             if stream is not None:
                 workspace.record_stream(stream)
-        wp, wn = c.vec(workspace, "workspace", need, torch.uint8), workspace.numel()
-    c.run("rms_norm_backward", stream, ctypes.byref(dy), _CODES[dY.dtype], ctypes.byref(h),
-          _CODES[H.dtype], w, _CODES[weight.dtype], rp, _ref(dh), ctypes.byref(dx),
-          _CODES[dX.dtype], dwp, wp, wn)
-
-
-def _teacher(c: _Call, S, teacher, idx):
-    return c.mat(S, "S"), c.mat(teacher, "teacher"), c.mat(idx, "idx", torch.int32)
+        wp, wn = _vec(workspace, "workspace", dev, need, torch.uint8), workspace.numel()
+    _run("rms_norm_backward", dev, stream, dy, _code(dY, "dY"), h, _code(H, "H"), w,
+         _code(weight, "weight"), rp, dh, dx, _code(dX, "dX"), dwp, wp, wn)
 
 
 def distill_loss(S: torch.Tensor, teacher: torch.Tensor, idx: torch.Tensor, loss: torch.Tensor,
                  lse: torch.Tensor, temperature: float = 1.0, stream=None) -> None:
     """loss <- tau^2 KL(softmax(teacher / tau) || softmax(S / tau) at idx) per
     row; lse <- the log of the student's normalizer."""
-    c = _Call()
-    s, t, i = _teacher(c, S, teacher, idx)
+    dev = S.get_device()
+    s, t, i = _mat(S, "S", dev), _mat(teacher, "teacher", dev), _mat(idx, "idx", dev, torch.int32)
     rows = S.shape[0]
-    lp, ep = c.vec(loss, "loss", rows), c.vec(lse, "lse", rows)
-    c.run("distill_loss", stream, ctypes.byref(s), _CODES[S.dtype], ctypes.byref(t),
-          _CODES[teacher.dtype], ctypes.byref(i), temperature, lp, ep)
+    _run("distill_loss", dev, stream, s, _code(S, "S"), t, _code(teacher, "teacher"), i,
+         temperature, _vec(loss, "loss", dev, rows), _vec(lse, "lse", dev, rows))
 
 
 def distill_loss_backward(S: torch.Tensor, teacher: torch.Tensor, idx: torch.Tensor,
                           lse: torch.Tensor, dloss: torch.Tensor, dS: torch.Tensor,
                           temperature: float = 1.0, stream=None) -> None:
     """dS <- the gradient of sum_t dloss_t loss_t with respect to S."""
-    c = _Call()
-    s, t, i = _teacher(c, S, teacher, idx)
+    dev = S.get_device()
+    s, t, i = _mat(S, "S", dev), _mat(teacher, "teacher", dev), _mat(idx, "idx", dev, torch.int32)
     rows = S.shape[0]
-    ep, gp = c.vec(lse, "lse", rows), c.vec(dloss, "dloss", rows)
-    d = c.mat(dS, "dS")
-    c.run("distill_loss_backward", stream, ctypes.byref(s), _CODES[S.dtype], ctypes.byref(t),
-          _CODES[teacher.dtype], ctypes.byref(i), temperature, ep, gp, ctypes.byref(d),
-          _CODES[dS.dtype])
+    _run("distill_loss_backward", dev, stream, s, _code(S, "S"), t, _code(teacher, "teacher"), i,
+         temperature, _vec(lse, "lse", dev, rows), _vec(dloss, "dloss", dev, rows),
+         _mat(dS, "dS", dev), _code(dS, "dS"))
