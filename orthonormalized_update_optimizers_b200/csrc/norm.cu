@@ -11,8 +11,6 @@
 namespace ouo {
 namespace {
 
-constexpr int kNThreads = 256;
-
 struct NormArgs {
   const void* X; int64_t ldx; int x_bf16;
   const void* R; int64_t ldr;
@@ -23,46 +21,127 @@ struct NormArgs {
   float* rstd;
   int64_t rows, cols;
   float eps;
+  int vx, vr, vh, vw, vy, vq;  // 16-byte (vq: 8-byte) accesses allowed
 };
 
 __device__ __forceinline__ const char* row_of(const void* p, int64_t r, int64_t ld, int bf16) {
   return reinterpret_cast<const char*>(p) + r * ld * (bf16 ? 2 : 4);
 }
 
-__global__ void __launch_bounds__(kNThreads) rms_kernel(const __grid_constant__ NormArgs a) {
+// A team per row, h in registers (as the values that H's type holds): x and
+// the residual are read once, and nothing is read back.
+template <int TPR, int NV>
+__global__ void __launch_bounds__(kTeamThreads<TPR>) rms_kernel(const __grid_constant__ NormArgs a) {
+  constexpr int kWarps = kTeamThreads<TPR> / 32, kTeams = kTeamThreads<TPR> / TPR;
+  __shared__ float reds[kWarps];
+  __shared__ uint32_t redm[kWarps];
+  const int64_t row = (int64_t)blockIdx.x * kTeams + (kTeams > 1 ? threadIdx.x / TPR : 0);
+  if (kTeams > 1 && row >= a.rows) return;
+  const int t = threadIdx.x % TPR, n = (int)a.cols;
+  RowRaw<TPR, NV> xr, rr;
+  float v[NV][8];
+  xr.load(row_of(a.X, row, a.ldx, a.x_bf16), t, n, a.x_bf16, a.vx);
+  if (a.R) rr.load(row_of(a.R, row, a.ldr, a.h_bf16), t, n, a.h_bf16, a.vr);
+  xr.get(v);
+  if (a.R) {
+    float u[NV][8];
+    rr.get(u);
+#pragma unroll
+    for (int c = 0; c < NV; ++c)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[c][i] += u[c][i];
+  }
+  if (a.H) {
+    char* h = const_cast<char*>(row_of(a.H, row, a.ldh, a.h_bf16));
+#pragma unroll
+    for (int c = 0; c < NV; ++c) {
+      row_st8(h, 8 * (t + c * TPR), n, a.h_bf16, a.vh, v[c]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[c][i] = round_to(v[c][i], a.h_bf16);
+    }
+  }
+  float acc = 0.f;
+#pragma unroll
+  for (int c = 0; c < NV; ++c)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc = fmaf(v[c][i], v[c][i], acc);
+  const float rstd = __frsqrt_rn(team_sum<TPR>(acc, reds) / (float)n + a.eps);
+  if (a.rstd && t == 0) a.rstd[row] = rstd;
+  uint32_t m = 0;
+#pragma unroll
+  for (int c = 0; c < NV; ++c) {
+    float w[8];
+    row_ld8(a.W, 8 * (t + c * TPR), n, a.w_bf16, a.vw, w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      v[c][i] = v[c][i] * rstd * w[i];
+      m = max(m, mag(v[c][i]));
+    }
+  }
+  if (a.Y) {
+    char* y = const_cast<char*>(row_of(a.Y, row, a.ldy, a.y_bf16));
+#pragma unroll
+    for (int c = 0; c < NV; ++c) row_st8(y, 8 * (t + c * TPR), n, a.y_bf16, a.vy, v[c]);
+  }
+  if (!a.Q) return;
+  const Quant q = quant_of(team_max<TPR>(m, redm));
+  if (t == 0) a.scale[row] = q.scale;
+#pragma unroll
+  for (int c = 0; c < NV; ++c)
+    row_stq(a.Q + row * a.ldq, 8 * (t + c * TPR), n, a.vq, quant8(v[c], q));
+}
+
+// Rows too long for registers: one block per row; h is read back (from H, or
+// from X when there is none) for each of the later passes.
+__global__ void __launch_bounds__(512) rms_long_kernel(const __grid_constant__ NormArgs a) {
   __shared__ uint32_t red[32];
-  const int64_t n = a.cols;
-  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
-    const char* x = row_of(a.X, row, a.ldx, a.x_bf16);
-    const char* rs = a.R ? row_of(a.R, row, a.ldr, a.h_bf16) : nullptr;
-    char* h = a.H ? const_cast<char*>(row_of(a.H, row, a.ldh, a.h_bf16)) : nullptr;
-    auto value = [&](int64_t j) {  // h, once written
-      return h ? ld1(h, j, a.h_bf16) : ld1(x, j, a.x_bf16);
-    };
-    float acc = 0.f;
-    for (int64_t j = threadIdx.x; j < n; j += kNThreads) {
-      float v = ld1(x, j, a.x_bf16);
-      if (rs) v += ld1(rs, j, a.h_bf16);
-      if (h) {
-        st1(h, j, v, a.h_bf16);
-        v = round_to(v, a.h_bf16);
-      }
-      acc = fmaf(v, v, acc);
+  const int n = (int)a.cols;
+  const int64_t row = blockIdx.x;
+  const char* x = row_of(a.X, row, a.ldx, a.x_bf16);
+  const char* rs = a.R ? row_of(a.R, row, a.ldr, a.h_bf16) : nullptr;
+  char* h = a.H ? const_cast<char*>(row_of(a.H, row, a.ldh, a.h_bf16)) : nullptr;
+  float acc = 0.f;
+  for (int j = 8 * threadIdx.x; j < n; j += 8 * 512) {
+    float v[8], u[8];
+    row_ld8(x, j, n, a.x_bf16, a.vx, v);
+    if (rs) {
+      row_ld8(rs, j, n, a.h_bf16, a.vr, u);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] += u[i];
     }
-    acc = block_sum(acc, reinterpret_cast<float*>(red));
-    const float rstd = __frsqrt_rn(acc / (float)n + a.eps);
-    if (a.rstd && threadIdx.x == 0) a.rstd[row] = rstd;
-    uint32_t m = 0;
-    for (int64_t j = threadIdx.x; j < n; j += kNThreads) {
-      const float y = value(j) * rstd * ld1(a.W, j, a.w_bf16);
-      m = max(m, mag(y));
-      if (a.Y) st1(const_cast<char*>(row_of(a.Y, row, a.ldy, a.y_bf16)), j, y, a.y_bf16);
+    if (h) row_st8(h, j, n, a.h_bf16, a.vh, v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (h) v[i] = round_to(v[i], a.h_bf16);
+      acc = fmaf(v[i], v[i], acc);
     }
-    if (!a.Q) continue;
-    const Quant q = quant_of(block_max(m, red));
-    if (threadIdx.x == 0) a.scale[row] = q.scale;
-    for (int64_t j = threadIdx.x; j < n; j += kNThreads)
-      a.Q[row * a.ldq + j] = (int8_t)quant1(value(j) * rstd * ld1(a.W, j, a.w_bf16), q);
+  }
+  const float rstd = __frsqrt_rn(block_sum(acc, reinterpret_cast<float*>(red)) / (float)n + a.eps);
+  if (a.rstd && threadIdx.x == 0) a.rstd[row] = rstd;
+  auto value = [&](int j, float v[8]) {
+    float w[8];
+    if (h) row_ld8(h, j, n, a.h_bf16, a.vh, v);
+    else row_ld8(x, j, n, a.x_bf16, a.vx, v);
+    row_ld8(a.W, j, n, a.w_bf16, a.vw, w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = v[i] * rstd * w[i];
+  };
+  uint32_t m = 0;
+  for (int j = 8 * threadIdx.x; j < n; j += 8 * 512) {
+    float v[8];
+    value(j, v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, mag(v[i]));
+    if (a.Y)
+      row_st8(const_cast<char*>(row_of(a.Y, row, a.ldy, a.y_bf16)), j, n, a.y_bf16, a.vy, v);
+  }
+  if (!a.Q) return;
+  const Quant q = quant_of(block_max(m, red));
+  if (threadIdx.x == 0) a.scale[row] = q.scale;
+  for (int j = 8 * threadIdx.x; j < n; j += 8 * 512) {
+    float v[8];
+    value(j, v);
+    row_stq(a.Q + row * a.ldq, j, n, a.vq, quant8(v, q));
   }
 }
 
@@ -75,16 +154,79 @@ struct NormBwdArgs {
   void* dX; int64_t lddx; int dx_bf16;
   float* part;
   int64_t rows, cols;
+  int vdy, vh, vw, vdh, vdx;  // 16-byte accesses allowed
 };
 
-// Block b takes rows b, b + grid, ...; its share of dw goes to row b of the
-// partial sums (each thread keeps its own columns, so nothing races).
-__global__ void __launch_bounds__(kNThreads) rms_bwd_kernel(const __grid_constant__ NormBwdArgs a) {
+// A block of TPR threads takes rows b, b + grid, ...; every thread keeps the
+// same columns of all of them, so that its share of dw stays in registers
+// and leaves once, to row b of the partial sums. 
+template <int TPR, int NV>
+__global__ void __launch_bounds__(TPR) rms_bwd_kernel(const __grid_constant__ NormBwdArgs a) {
+  __shared__ float red[2][TPR / 32];
+  const int t = threadIdx.x, n = (int)a.cols;
+  float w[NV][8], dw[NV][8], g[NV][8], h[NV][8];
+#pragma unroll
+  for (int c = 0; c < NV; ++c) {
+    row_ld8(a.W, 8 * (t + c * TPR), n, a.w_bf16, a.vw, w[c]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) dw[c][i] = 0.f;
+  }
+  const float inv_n = 1.f / (float)n;
+  int flip = 0;
+  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, flip ^= 1) {
+    const float r = a.rstd[row];
+    const char* dy = row_of(a.dY, row, a.lddy, a.dy_bf16);
+    const char* hp = row_of(a.H, row, a.ldh, a.h_bf16);
+    const char* dh = a.dH ? row_of(a.dH, row, a.lddh, a.dx_bf16) : nullptr;
+    float acc = 0.f;
+    RowRaw<TPR, NV> gr, hr, dr;
+    gr.load(dy, t, n, a.dy_bf16, a.vdy);
+    hr.load(hp, t, n, a.h_bf16, a.vh);
+    if (dh) dr.load(dh, t, n, a.dx_bf16, a.vdh);
+    gr.get(g);
+    hr.get(h);
+#pragma unroll
+    for (int c = 0; c < NV; ++c)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        h[c][i] *= r;
+        dw[c][i] = fmaf(g[c][i], h[c][i], dw[c][i]);
+        g[c][i] *= w[c][i];
+        acc = fmaf(g[c][i], h[c][i], acc);
+      }
+    const float m = team_sum<TPR>(acc, red[flip]) * inv_n;
+    char* dx = const_cast<char*>(row_of(a.dX, row, a.lddx, a.dx_bf16));
+#pragma unroll
+    for (int c = 0; c < NV; ++c)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) g[c][i] = r * (g[c][i] - h[c][i] * m);
+    if (dh) {
+      dr.get(h);
+#pragma unroll
+      for (int c = 0; c < NV; ++c)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) g[c][i] += h[c][i];
+    }
+#pragma unroll
+    for (int c = 0; c < NV; ++c)
+      row_st8(dx, 8 * (t + c * TPR), n, a.dx_bf16, a.vdx, g[c]);
+  }
+  if (a.part) {
+    float* part = a.part + blockIdx.x * a.cols;
+#pragma unroll
+    for (int c = 0; c < NV; ++c)
+      row_st8(part, 8 * (t + c * TPR), n, 0, n % 4 == 0, dw[c]);
+  }
+}
+
+// Rows too long for registers: dw's shares stay in the partial sums, where
+// each thread adds to its own columns.
+__global__ void __launch_bounds__(512) rms_bwd_long_kernel(const __grid_constant__ NormBwdArgs a) {
   __shared__ uint32_t red[32];
-  const int64_t n = a.cols;
-  float* part = a.part ? a.part + blockIdx.x * n : nullptr;
+  const int n = (int)a.cols;
+  float* part = a.part ? a.part + blockIdx.x * a.cols : nullptr;
   if (part)
-    for (int64_t j = threadIdx.x; j < n; j += kNThreads) part[j] = 0.f;
+    for (int j = threadIdx.x; j < n; j += 512) part[j] = 0.f;
   for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
     const char* dy = row_of(a.dY, row, a.lddy, a.dy_bf16);
     const char* h = row_of(a.H, row, a.ldh, a.h_bf16);
@@ -92,13 +234,13 @@ __global__ void __launch_bounds__(kNThreads) rms_bwd_kernel(const __grid_constan
     char* dx = const_cast<char*>(row_of(a.dX, row, a.lddx, a.dx_bf16));
     const float r = a.rstd[row];
     float acc = 0.f;
-    for (int64_t j = threadIdx.x; j < n; j += kNThreads) {
+    for (int j = threadIdx.x; j < n; j += 512) {
       const float g = ld1(dy, j, a.dy_bf16), xh = ld1(h, j, a.h_bf16) * r;
       acc = fmaf(g * ld1(a.W, j, a.w_bf16), xh, acc);
       if (part) part[j] = fmaf(g, xh, part[j]);
     }
     const float c = block_sum(acc, reinterpret_cast<float*>(red)) / (float)n;
-    for (int64_t j = threadIdx.x; j < n; j += kNThreads) {
+    for (int j = threadIdx.x; j < n; j += 512) {
       const float g = ld1(dy, j, a.dy_bf16) * ld1(a.W, j, a.w_bf16);
       float v = r * (g - ld1(h, j, a.h_bf16) * r * c);
       if (dh) v += ld1(dh, j, a.dx_bf16);
@@ -107,14 +249,23 @@ __global__ void __launch_bounds__(kNThreads) rms_bwd_kernel(const __grid_constan
   }
 }
 
-// dw = sum of the partial rows, in a fixed order.
-__global__ void __launch_bounds__(256)
+// dw = sum of the partial rows, in a fixed order: 16 threads a column, each
+// every 16th row, then their sums.
+__global__ void __launch_bounds__(512)
 rms_dw_kernel(const float* part, int nparts, int64_t cols, float* dw) {
-  const int64_t j = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (j >= cols) return;
+  __shared__ float sum[16][33];
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int64_t j = (int64_t)blockIdx.x * 32 + lane;
   float v = 0.f;
-  for (int p = 0; p < nparts; ++p) v += part[p * cols + j];
-  dw[j] = v;
+  if (j < cols)
+    for (int p = w; p < nparts; p += 16) v += part[p * cols + j];
+  sum[w][lane] = v;
+  __syncthreads();
+  if (w == 0 && j < cols) {
+#pragma unroll
+    for (int i = 1; i < 16; ++i) v += sum[i][lane];
+    dw[j] = v;
+  }
 }
 
 // Rows of partial sums of dw: a function of the shape alone, so that the
@@ -173,10 +324,26 @@ int rms_norm(const ouo_mat* X, int x_dtype, const ouo_mat* residual, const ouo_m
   if (Q) { a.Q = (int8_t*)Q->ptr; a.ldq = Q->ld; a.scale = scale; }
   a.rstd = rstd;
   a.rows = T; a.cols = n; a.eps = eps;
-  const int64_t cap = (int64_t)num_sms() * 8;
-  rms_kernel<<<(unsigned)(T < cap ? T : cap), kNThreads, 0, (cudaStream_t)stream>>>(a);
-  OUO_CHECK_LAUNCH();
-  return OUO_OK;
+  a.vx = rows16(*X, elem_size(x_dtype));
+  a.vr = residual ? rows16(*residual, elem_size(h_dtype)) : 0;
+  a.vh = H ? rows16(*H, elem_size(h_dtype)) : 0;
+  a.vw = (uintptr_t)weight % 16 == 0;
+  a.vy = Y ? rows16(*Y, elem_size(y_dtype)) : 0;
+  a.vq = Q ? (uintptr_t)a.Q % 8 == 0 && (T <= 1 || a.ldq % 8 == 0) : 0;
+  cudaStream_t s = (cudaStream_t)stream;
+  const Team t = team_for(T, n);
+  if (t.tpr == 0) {
+    rms_long_kernel<<<(unsigned)T, 512, 0, s>>>(a);
+    OUO_CHECK_LAUNCH();
+    return OUO_OK;
+  }
+  return with_team(t, [&](auto tpr, auto nv) -> int {
+    constexpr int TPR = decltype(tpr)::value, NV = decltype(nv)::value;
+    constexpr int kTeams = kTeamThreads<TPR> / TPR;
+    rms_kernel<TPR, NV><<<(unsigned)ceil_div(T, (int64_t)kTeams), kTeamThreads<TPR>, 0, s>>>(a);
+    OUO_CHECK_LAUNCH();
+    return OUO_OK;
+  });
 }
 
 size_t rms_norm_backward_workspace_bytes(int64_t rows, int64_t cols) {
@@ -226,11 +393,20 @@ int rms_norm_backward(const ouo_mat* dY, int dy_dtype, const ouo_mat* H, int h_d
     a.dX = dX->ptr; a.lddx = dX->ld; a.dx_bf16 = dx_dtype == OUO_BF16;
     a.part = dweight ? (float*)ws : nullptr;
     a.rows = T; a.cols = n;
-    rms_bwd_kernel<<<(unsigned)parts, kNThreads, 0, s>>>(a);
+    a.vdy = rows16(*dY, elem_size(dy_dtype));
+    a.vh = rows16(*H, elem_size(h_dtype));
+    a.vw = (uintptr_t)weight % 16 == 0;
+    a.vdh = dH ? rows16(*dH, elem_size(dx_dtype)) : 0;
+    a.vdx = rows16(*dX, elem_size(dx_dtype));
+    const unsigned grid = (unsigned)parts;
+    if (n <= 128 * 8) rms_bwd_kernel<128, 1><<<grid, 128, 0, s>>>(a);
+    else if (n <= 512 * 8) rms_bwd_kernel<512, 1><<<grid, 512, 0, s>>>(a);
+    else if (n <= 512 * 16) rms_bwd_kernel<512, 2><<<grid, 512, 0, s>>>(a);
+    else rms_bwd_long_kernel<<<grid, 512, 0, s>>>(a);
     OUO_CHECK_LAUNCH();
   }
   if (dweight && n > 0) {
-    rms_dw_kernel<<<(unsigned)ceil_div(n, 256), 256, 0, s>>>((const float*)ws, (int)parts, n,
+    rms_dw_kernel<<<(unsigned)ceil_div(n, 32), 512, 0, s>>>((const float*)ws, (int)parts, n,
                                                              dweight);
     OUO_CHECK_LAUNCH();
   }

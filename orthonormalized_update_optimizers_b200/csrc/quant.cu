@@ -4,12 +4,14 @@
 //   scale_i = max_j |x_ij| / 127,  q_ij = rint(x_ij / scale_i)
 //
 // HBM-bound: each element is read once and leaves as one byte.
+#include <cstring>
+#include <mutex>
+
 #include "tokens.cuh"
+#include "umma.cuh"
 
 namespace ouo {
 namespace {
-
-constexpr int kQThreads = 256;
 
 struct QuantArgs {
   int nmat, bf16;
@@ -20,58 +22,290 @@ struct QuantArgs {
   int8_t* Q[kChunk];
   int64_t ldq[kChunk];
   float* scale[kChunk];
+  uint8_t vecx[kChunk], vecq[kChunk];
 };
 
-// One block per row: largest magnitude, then the rounding (the second read
-// comes from the caches).
-__global__ void __launch_bounds__(kQThreads) quant_rows_kernel(const __grid_constant__ QuantArgs a) {
+// Matrix of a launch-wide row.
+__device__ __forceinline__ int matrix_of(const QuantArgs& a, int64_t row) {
+  int lo = 0, hi = a.nmat - 1;
+  while (lo < hi) {
+    int mid = (lo + hi + 1) >> 1;
+    if (a.row_start[mid] <= row) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+
+// A team per row, the row in registers: one read, one write.
+template <int TPR, int NV>
+__global__ void __launch_bounds__(kTeamThreads<TPR>)
+quant_rows_kernel(const __grid_constant__ QuantArgs a) {
+  __shared__ uint32_t red[kTeamThreads<TPR> / 32];
+  constexpr int kTeams = kTeamThreads<TPR> / TPR;
+  const int64_t row = (int64_t)blockIdx.x * kTeams + (kTeams > 1 ? threadIdx.x / TPR : 0);
+  if (kTeams > 1 && row >= a.row_start[a.nmat]) return;
+  const int t = threadIdx.x % TPR;
+  const int g = matrix_of(a, row);
+  const int64_t r = row - a.row_start[g];
+  const int n = (int)a.cols[g];
+  const char* x = reinterpret_cast<const char*>(a.X[g]) + r * a.ldx[g] * (a.bf16 ? 2 : 4);
+  RowRaw<TPR, NV> raw;
+  float v[NV][8];
+  raw.load(x, t, n, a.bf16, a.vecx[g]);
+  raw.get(v);
+  uint32_t m = 0;
+#pragma unroll
+  for (int c = 0; c < NV; ++c)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, mag(v[c][i]));
+  const Quant q = quant_of(team_max<TPR>(m, red));
+  if (t == 0) a.scale[g][r] = q.scale;
+  int8_t* o = a.Q[g] + r * a.ldq[g];
+#pragma unroll
+  for (int c = 0; c < NV; ++c) row_stq(o, 8 * (t + c * TPR), n, a.vecq[g], quant8(v[c], q));
+}
+
+// Rows too long for registers: one block per row, read twice (the second
+// time from the caches).
+__global__ void __launch_bounds__(512) quant_long_kernel(const __grid_constant__ QuantArgs a) {
   __shared__ uint32_t red[32];
-  const int64_t total = a.row_start[a.nmat];
-  for (int64_t row = blockIdx.x; row < total; row += gridDim.x) {
-    int lo = 0, hi = a.nmat - 1;
-    while (lo < hi) {
-      int mid = (lo + hi + 1) >> 1;
-      if (a.row_start[mid] <= row) lo = mid; else hi = mid - 1;
-    }
-    const int64_t r = row - a.row_start[lo], n = a.cols[lo];
-    const char* x = reinterpret_cast<const char*>(a.X[lo]) + r * a.ldx[lo] * (a.bf16 ? 2 : 4);
-    uint32_t m = 0;
-    for (int64_t j = threadIdx.x; j < n; j += kQThreads) m = max(m, mag(ld1(x, j, a.bf16)));
-    m = block_max(m, red);
-    const Quant q = quant_of(m);
-    if (threadIdx.x == 0) a.scale[lo][r] = q.scale;
-    int8_t* o = a.Q[lo] + r * a.ldq[lo];
-    for (int64_t j = threadIdx.x; j < n; j += kQThreads) o[j] = (int8_t)quant1(ld1(x, j, a.bf16), q);
+  const int64_t row = blockIdx.x;
+  const int g = matrix_of(a, row);
+  const int64_t r = row - a.row_start[g];
+  const int64_t n = a.cols[g];
+  const char* x = reinterpret_cast<const char*>(a.X[g]) + r * a.ldx[g] * (a.bf16 ? 2 : 4);
+  int8_t* o = a.Q[g] + r * a.ldq[g];
+  uint32_t m = 0;
+  for (int64_t j = 8 * threadIdx.x; j < n; j += 8 * 512) {
+    float v[8];
+    row_ld8(x, (int)j, (int)n, a.bf16, a.vecx[g], v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, mag(v[i]));
+  }
+  const Quant q = quant_of(block_max(m, red));
+  if (threadIdx.x == 0) a.scale[g][r] = q.scale;
+  for (int64_t j = 8 * threadIdx.x; j < n; j += 8 * 512) {
+    float v[8];
+    row_ld8(x, (int)j, (int)n, a.bf16, a.vecx[g], v);
+    row_stq(o, (int)j, (int)n, a.vecq[g], quant8(v, q));
   }
 }
 
-// Transposed: one block per 32 columns of one matrix.
-__global__ void __launch_bounds__(256)
-quant_cols_kernel(const void* X, int bf16, int64_t rows, int64_t cols, int64_t ldx, int8_t* Q,
-                  int64_t ldq, float* scale) {
-  __shared__ uint32_t amax[8][33];
-  __shared__ int8_t tile[32][36];
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const int64_t c = (int64_t)blockIdx.x * 32 + lane;
-  uint32_t m = 0;
-  if (c < cols)
-    for (int64_t r = w; r < rows; r += 8) m = max(m, mag(ld1(X, r * ldx + c, bf16)));
-  amax[w][lane] = m;
-  __syncthreads();
-  for (int i = 0; i < 8; ++i) m = max(m, amax[i][lane]);
-  const Quant q = quant_of(m);
-  if (w == 0 && c < cols) scale[c] = q.scale;
-  for (int64_t r0 = 0; r0 < rows; r0 += 32) {
-    for (int i = w; i < 32; i += 8)
-      tile[lane][i] = c < cols && r0 + i < rows
-          ? (int8_t)quant1(ld1(X, (r0 + i) * ldx + c, bf16), q) : (int8_t)0;
-    __syncthreads();
-    for (int i = w; i < 32; i += 8) {
-      const int64_t oc = (int64_t)blockIdx.x * 32 + i;
-      if (oc < cols && r0 + lane < rows) Q[oc * ldq + r0 + lane] = tile[i][lane];
-    }
-    __syncthreads();
+// Transposed.  A cluster of CTAs takes a strip of 64 bytes of columns and
+// divides its rows; every CTA keeps its rows in shared memory (as many as
+// fit) while it looks for the columns' largest magnitudes, the cluster joins
+// those through distributed shared memory, and the CTA writes its rows' share
+// of the strip's transpose.  So X is read once (rows past what fits, twice),
+// in one launch and without a workspace.
+constexpr int kTThreads = 256;
+constexpr int kSegBytes = 64;  // of a row in one strip: 32 bf16 or 16 fp32 columns
+constexpr int kMaxCluster = 8;
+
+struct QuantTArgs {
+  const void* X;
+  int64_t rows, cols, ldx;
+  int8_t* Q;
+  int64_t ldq;
+  float* scale;
+  int vecx, vecq;
+  int64_t rows_cta;  // a multiple of 32
+  int cached;        // rows of a CTA that stay in shared memory, a multiple of 32
+};
+
+// 16 bytes of row r: columns c .. c + 16 / ES - 1, zero outside the matrix.
+template <int BF>
+__device__ __forceinline__ uint4 seg_ld(const QuantTArgs& a, int64_t r, int64_t c) {
+  constexpr int kE = BF ? 8 : 4;
+  const char* p = reinterpret_cast<const char*>(a.X) + (r * a.ldx + c) * (BF ? 2 : 4);
+  if (a.vecx && c + kE <= a.cols) return *reinterpret_cast<const uint4*>(p);
+  uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int i = 0; i < kE; ++i) {
+    if (c + i >= a.cols) break;
+    if (BF) w[i >> 1] |= (uint32_t)reinterpret_cast<const uint16_t*>(p)[i] << (16 * (i & 1));
+    else w[i] = reinterpret_cast<const uint32_t*>(p)[i];
   }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+template <int BF>
+__global__ void __launch_bounds__(kTThreads)
+quant_cols_kernel(const __grid_constant__ QuantTArgs a) {
+  constexpr int kCols = BF ? 32 : 16;  // of the strip
+  extern __shared__ __align__(16) uint32_t cache[];  // [cached][16 words]
+  __shared__ uint32_t wmax[kTThreads / 32][kCols];
+  __shared__ uint32_t cmax[kCols];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint32_t nct;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(nct));
+  const uint32_t rank = ptx::cluster_ctarank();
+  const int64_t strip = blockIdx.x / nct;
+  const int64_t c0 = strip * kCols;
+  const int64_t ra = rank * a.rows_cta;
+  const int64_t rb = ra + a.rows_cta < a.rows ? ra + a.rows_cta : a.rows;
+  // columns' largest magnitudes: four threads per row, 16 bytes each
+  const int seg = threadIdx.x & 3;
+  uint32_t m[BF ? 8 : 4];
+#pragma unroll
+  for (int i = 0; i < (BF ? 8 : 4); ++i) m[i] = 0;
+  auto take = [&](const uint4& u) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (BF) {
+        m[2 * i] = max(m[2 * i], (w[i] << 16) & 0x7fffffffu);
+        m[2 * i + 1] = max(m[2 * i + 1], w[i] & 0x7fff0000u);
+      } else {
+        m[i] = max(m[i], w[i] & 0x7fffffffu);
+      }
+    }
+  };
+  constexpr int kRowsPass = kTThreads / 4, kU = 8;
+  for (int64_t r = ra + (threadIdx.x >> 2); r < rb; r += kRowsPass * kU) {
+    uint4 u[kU];
+#pragma unroll
+    for (int k = 0; k < kU; ++k)
+      u[k] = r + k * kRowsPass < rb ? seg_ld<BF>(a, r + k * kRowsPass, c0 + seg * (16 / (BF ? 2 : 4)))
+                                    : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int k = 0; k < kU; ++k) {
+      take(u[k]);
+      const int64_t l = r + k * kRowsPass - ra;
+      if (l < a.cached) reinterpret_cast<uint4*>(cache)[l * 4 + seg] = u[k];
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < (BF ? 8 : 4); ++i) {
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) m[i] = max(m[i], __shfl_xor_sync(0xffffffffu, m[i], o));
+    if (lane < 4) wmax[warp][seg * (BF ? 8 : 4) + i] = m[i];
+  }
+  __syncthreads();
+  if (threadIdx.x < kCols) {
+    uint32_t v = 0;
+#pragma unroll
+    for (int w = 0; w < kTThreads / 32; ++w) v = max(v, wmax[w][threadIdx.x]);
+    cmax[threadIdx.x] = v;
+  }
+  __syncwarp();
+  ptx::cluster_sync();
+  // every thread's one or two columns: word `wd` of a row
+  const int wd = lane & 15, half = lane >> 4;
+  uint32_t x0 = 0, x1 = 0;
+  for (uint32_t p = 0; p < nct; ++p) {
+    x0 = max(x0, (uint32_t)ptx::ld_cluster_int(
+                     ptx::mapa(ptx::smem_u32(&cmax[BF ? 2 * wd : wd]), p)));
+    if (BF)
+      x1 = max(x1, (uint32_t)ptx::ld_cluster_int(ptx::mapa(ptx::smem_u32(&cmax[2 * wd + 1]), p)));
+  }
+  __syncwarp();
+  ptx::cluster_sync();  // everyone has read everyone's (nothing is read from afar below)
+  const Quant q0 = quant_of(x0), q1 = quant_of(x1);
+  const int64_t col = c0 + (BF ? 2 * wd : wd);
+  if (rank == 0 && warp == 0 && half == 0) {
+    if (col < a.cols) a.scale[col] = q0.scale;
+    if (BF && col + 1 < a.cols) a.scale[col + 1] = q1.scale;
+  }
+  // 32 rows per warp and pass; a half warp takes 16 of them, each lane a word
+  // of every row.  The halves read rows of opposite parity, so that their 16
+  // words lie in different banks.
+  for (int64_t base = ra + warp * 32; base < rb; base += kTThreads) {
+    const int64_t r0 = base + 16 * half;
+    uint32_t w[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int k = i ^ 1;  // the other half's row of this step
+      const int64_t l = r0 - ra + (half ? k : i);
+      uint32_t v = 0;
+      if (l < a.cached) {
+        v = cache[l * 16 + wd];
+      } else if (ra + l < rb) {
+        if (BF) {
+          if (col < a.cols)
+            v = reinterpret_cast<const uint16_t*>(a.X)[(ra + l) * a.ldx + col];
+          if (col + 1 < a.cols)
+            v |= (uint32_t)reinterpret_cast<const uint16_t*>(a.X)[(ra + l) * a.ldx + col + 1] << 16;
+        } else if (col < a.cols) {
+          v = reinterpret_cast<const uint32_t*>(a.X)[(ra + l) * a.ldx + col];
+        }
+      }
+      w[i] = v;
+    }
+    if (half) {
+#pragma unroll
+      for (int i = 0; i < 16; i += 2) {
+        const uint32_t s = w[i];
+        w[i] = w[i + 1];
+        w[i + 1] = s;
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < (BF ? 2 : 1); ++e) {
+      float v[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        v[i] = __uint_as_float(!BF ? w[i] : e ? w[i] & 0xffff0000u : w[i] << 16);
+      const Quant& q = e ? q1 : q0;
+      const uint2 lo = quant8(v, q), hi = quant8(v + 8, q);
+      if (col + e >= a.cols || r0 >= rb) continue;
+      int8_t* o = a.Q + (col + e) * a.ldq;
+      if (a.vecq && r0 + 16 <= rb) {
+        *reinterpret_cast<uint4*>(o + r0) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+      } else {
+        const uint32_t b[4] = {lo.x, lo.y, hi.x, hi.y};
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if (r0 + i < rb) o[r0 + i] = (int8_t)((b[i >> 2] >> (8 * (i & 3))) & 255u);
+      }
+    }
+  }
+}
+
+template <int BF>
+int quant_cols(const ouo_mat& X, const ouo_mat& Q, float* scale, cudaStream_t s) {
+  // shared memory for two CTAs a SM; below 256 rows a CTA the cluster shrinks
+  constexpr int kCached = 1600;
+  constexpr size_t kSmem = (size_t)kCached * kSegBytes;
+  static std::mutex mu;
+  static bool ready[64] = {false};
+  int dev = 0;
+  OUO_CHECK_CUDA(cudaGetDevice(&dev));
+  if (dev < 0 || dev >= 64)
+    return set_error(OUO_ERR_UNSUPPORTED, "device ordinal %d out of range", dev);
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (!ready[dev]) {
+      OUO_CHECK_CUDA(cudaFuncSetAttribute(quant_cols_kernel<BF>,
+                                          cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem));
+      ready[dev] = true;
+    }
+  }
+  unsigned cluster = 1;
+  while (cluster < kMaxCluster && ceil_div(X.rows, (int64_t)2 * cluster) >= 128) cluster *= 2;
+  QuantTArgs a;
+  a.X = X.ptr; a.rows = X.rows; a.cols = X.cols; a.ldx = X.ld;
+  a.Q = (int8_t*)Q.ptr; a.ldq = Q.ld;
+  a.scale = scale;
+  a.vecx = rows16(X, BF ? 2 : 4);
+  a.vecq = rows16(Q, 1);
+  a.rows_cta = ceil_div(ceil_div(X.rows, (int64_t)cluster), 32) * 32;
+  a.cached = (int)(a.rows_cta < kCached ? a.rows_cta : kCached);
+  const int64_t strips = ceil_div(X.cols, (int64_t)(BF ? 32 : 16));
+  cudaLaunchConfig_t cfg;
+  memset(&cfg, 0, sizeof(cfg));
+  cfg.gridDim = dim3((unsigned)(strips * cluster), 1, 1);
+  cfg.blockDim = dim3(kTThreads, 1, 1);
+  cfg.dynamicSmemBytes = (size_t)a.cached * kSegBytes;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cluster;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  OUO_CHECK_CUDA(cudaLaunchKernelEx(&cfg, quant_cols_kernel<BF>, a));
+  OUO_CHECK_LAUNCH();
+  return OUO_OK;
 }
 
 }  // namespace
@@ -101,18 +335,17 @@ extern "C" int quantize_int8(const ouo_mat* X, int x_dtype, const ouo_mat* Q, fl
   if (transpose) {
     for (int i = 0; i < nmat; ++i) {
       if (X[i].cols == 0) continue;
-      quant_cols_kernel<<<(unsigned)ceil_div(X[i].cols, 32), 256, 0, s>>>(
-          X[i].ptr, bf16, X[i].rows, X[i].cols, X[i].ld, (int8_t*)Q[i].ptr, Q[i].ld, scale[i]);
-      OUO_CHECK_LAUNCH();
+      OUO_TRY(bf16 ? quant_cols<1>(X[i], Q[i], scale[i], s) : quant_cols<0>(X[i], Q[i], scale[i], s));
     }
     return OUO_OK;
   }
+  // One launch per kChunk matrices; the longest rows choose its teams.
   for (int c0 = 0; c0 < nmat; c0 += kChunk) {
     const int cn = nmat - c0 < kChunk ? nmat - c0 : kChunk;
     QuantArgs a;
     a.nmat = cn;
     a.bf16 = bf16;
-    int64_t acc = 0;
+    int64_t acc = 0, longest = 0;
     for (int i = 0; i < cn; ++i) {
       const ouo_mat& x = X[c0 + i];
       a.row_start[i] = acc;
@@ -122,13 +355,27 @@ extern "C" int quantize_int8(const ouo_mat* X, int x_dtype, const ouo_mat* Q, fl
       a.Q[i] = (int8_t*)Q[c0 + i].ptr;
       a.ldq[i] = Q[c0 + i].ld;
       a.scale[i] = scale[c0 + i];
+      a.vecx[i] = rows16(x, elem_size(x_dtype));
+      a.vecq[i] = (uintptr_t)a.Q[i] % 8 == 0 && (x.rows <= 1 || a.ldq[i] % 8 == 0);
       acc += x.rows;
+      if (x.rows > 0 && x.cols > longest) longest = x.cols;
     }
     a.row_start[cn] = acc;
     if (acc == 0) continue;
-    const int64_t cap = (int64_t)num_sms() * 8;
-    quant_rows_kernel<<<(unsigned)(acc < cap ? acc : cap), kQThreads, 0, s>>>(a);
-    OUO_CHECK_LAUNCH();
+    if (acc > 0x7fffffff) return set_error(OUO_ERR_UNSUPPORTED, "X: too many rows in one batch");
+    const Team t = team_for(acc, longest);
+    if (t.tpr == 0) {
+      quant_long_kernel<<<(unsigned)acc, 512, 0, s>>>(a);
+      OUO_CHECK_LAUNCH();
+      continue;
+    }
+    OUO_TRY(with_team(t, [&](auto tpr, auto nv) -> int {
+      constexpr int TPR = decltype(tpr)::value, NV = decltype(nv)::value;
+      constexpr int kTeams = kTeamThreads<TPR> / TPR;
+      quant_rows_kernel<TPR, NV><<<(unsigned)ceil_div(acc, (int64_t)kTeams), kTeamThreads<TPR>, 0, s>>>(a);
+      OUO_CHECK_LAUNCH();
+      return OUO_OK;
+    }));
   }
   return OUO_OK;
 }

@@ -4,6 +4,8 @@
 // rounding to 8 bits.
 #pragma once
 
+#include <type_traits>
+
 #include "internal.h"
 
 namespace ouo {
@@ -127,10 +129,162 @@ __device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t* red) {
   return v;
 }
 
+// ------------------------------------------------------------------ teams
+// A team of TPR threads (32, 128 or 512) holds one row of a matrix in
+// registers: chunk c of thread t is elements 8 (t + c TPR) .. + 7, NV chunks a
+// thread.  One read of the row then serves its norm, its largest magnitude
+// and its rounding.  A block is one team, or four of one warp each.
+template <int TPR>
+constexpr int kTeamThreads = TPR < 128 ? 128 : TPR;
+
+// Sum / maximum over a team.  `red` holds kTeamThreads / 32 words of shared
+// memory, one set per reduction in flight (two reductions in a row use two
+// sets, so that one barrier each is enough).
+template <int TPR>
+__device__ __forceinline__ float team_sum(float v, float* red) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if (TPR == 32) return v;
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = red[0];
+#pragma unroll
+  for (int i = 1; i < TPR / 32; ++i) v += red[i];
+  return v;
+}
+
+template <int TPR>
+__device__ __forceinline__ uint32_t team_max(uint32_t v, uint32_t* red) {
+  v = __reduce_max_sync(0xffffffffu, v);
+  if (TPR == 32) return v;
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = red[0];
+#pragma unroll
+  for (int i = 1; i < TPR / 32; ++i) v = max(v, red[i]);
+  return v;
+}
+
+// Chunk of 8 elements starting at j of a row of n; vec: 16-byte loads allowed.
+__device__ __forceinline__ void row_ld8(const void* p, int j, int n, int bf16, int vec,
+                                        float v[8]) {
+  if (vec && j + 8 <= n) {
+    ld8(p, j, bf16, v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = j + i < n ? ld1(p, j + i, bf16) : 0.f;
+  }
+}
+
+__device__ __forceinline__ void row_st8(void* p, int j, int n, int bf16, int vec,
+                                        const float v[8]) {
+  if (vec && j + 8 <= n) {
+    st8(p, j, bf16, v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (j + i < n) st1(p, j + i, v[i], bf16);
+  }
+}
+
+// A thread's chunks of one row, as they are stored.  Loading and converting
+// are separate, and each branches once on the element type: every load of the
+// row is in flight before the first one is waited for.
+template <int TPR, int NV>
+struct RowRaw {
+  uint4 a[NV], b[NV];  // b: the second half of fp32 chunks
+  int packed;          // a holds 8 bf16 (else a, b hold 8 fp32)
+
+  // fast: 16-byte accesses allowed and n a multiple of 8
+  __device__ __forceinline__ void load(const void* p, int t, int n, int bf16, int vec) {
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    if (vec && (n & 7) == 0) {
+      packed = bf16;
+      if (bf16) {
+        const uint4* q = reinterpret_cast<const uint4*>(p);
+#pragma unroll
+        for (int c = 0; c < NV; ++c) a[c] = 8 * (t + c * TPR) < n ? q[t + c * TPR] : zero;
+      } else {
+        const uint4* q = reinterpret_cast<const uint4*>(p);
+#pragma unroll
+        for (int c = 0; c < NV; ++c) {
+          const bool in = 8 * (t + c * TPR) < n;
+          a[c] = in ? q[2 * (t + c * TPR)] : zero;
+          b[c] = in ? q[2 * (t + c * TPR) + 1] : zero;
+        }
+      }
+    } else {
+      packed = 0;
+#pragma unroll
+      for (int c = 0; c < NV; ++c) {
+        float v[8];
+        row_ld8(p, 8 * (t + c * TPR), n, bf16, vec, v);
+        a[c] = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                          __float_as_uint(v[3]));
+        b[c] = make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]),
+                          __float_as_uint(v[7]));
+      }
+    }
+  }
+
+  __device__ __forceinline__ void get(float v[NV][8]) const {
+    if (packed) {
+#pragma unroll
+      for (int c = 0; c < NV; ++c) unpack8(a[c], v[c]);
+    } else {
+#pragma unroll
+      for (int c = 0; c < NV; ++c) {
+        v[c][0] = __uint_as_float(a[c].x); v[c][1] = __uint_as_float(a[c].y);
+        v[c][2] = __uint_as_float(a[c].z); v[c][3] = __uint_as_float(a[c].w);
+        v[c][4] = __uint_as_float(b[c].x); v[c][5] = __uint_as_float(b[c].y);
+        v[c][6] = __uint_as_float(b[c].z); v[c][7] = __uint_as_float(b[c].w);
+      }
+    }
+  }
+};
+
+// How a matrix of rows x cols is given to teams: enough threads per row that
+// a thread holds at most 8 chunks, and whole blocks per row where there are
+// too few rows to fill the GPU with warps (a row's latency counts then).
+// cols above 16384 do not fit: TPR 0.
+struct Team {
+  int tpr, nv;
+};
+
+inline Team team_for(int64_t rows, int64_t cols) {
+  const int64_t chunks = ceil_div(cols, (int64_t)8);
+  int tpr = chunks <= 32 * 8 ? 32 : chunks <= 128 * 8 ? 128 : 512;
+  if (chunks > 512 * 4) return Team{0, 0};
+  if (rows < 4 * num_sms()) tpr = chunks <= 128 ? (chunks <= 32 ? 32 : 128) : 512;
+  int nv = 1;
+  while ((int64_t)tpr * nv < chunks) nv *= 2;
+  return Team{tpr, nv};
+}
+
+template <int I>
+using C = std::integral_constant<int, I>;
+
+// f(C<TPR>, C<NV>) for the team's instance.
+template <class F>
+int with_team(Team t, F&& f) {
+  switch (t.tpr * 16 + t.nv) {
+    case 32 * 16 + 1: return f(C<32>{}, C<1>{});
+    case 32 * 16 + 2: return f(C<32>{}, C<2>{});
+    case 32 * 16 + 4: return f(C<32>{}, C<4>{});
+    case 32 * 16 + 8: return f(C<32>{}, C<8>{});
+    case 128 * 16 + 1: return f(C<128>{}, C<1>{});
+    case 128 * 16 + 4: return f(C<128>{}, C<4>{});
+    case 128 * 16 + 8: return f(C<128>{}, C<8>{});
+    case 512 * 16 + 1: return f(C<512>{}, C<1>{});
+    case 512 * 16 + 2: return f(C<512>{}, C<2>{});
+    default: return f(C<512>{}, C<4>{});
+  }
+}
+
 // 8-bit rounding of a row with the largest magnitude `amax`:
 //   scale = amax / 127,  q = rint(x * (127 / amax)).
-// The quotient 127 / amax is rounded once, so x * inv is within 1.5 ulp of
-// x / scale and q differs from the exact quotient's rounding only where that
+// The quotient 127 / amax is rounded once, so x * inv is within one rounding
+// of x / scale and q differs from the exact quotient's rounding only where that
 // lies within 1e-5 of a half.  Below 2^-96 the reciprocal could overflow:
 // there x and amax are multiplied by 2^96 (exact) first.  A zero row has scale
 // 0 and zeros; a row with a NaN or an infinity has scale NaN and zeros, so
@@ -154,15 +308,42 @@ __device__ __forceinline__ Quant quant_of(uint32_t amax_bits) {
   return q;
 }
 
+// The integer nearest to x * inv is in the low byte of x * inv + 1.5 * 2^23,
+// an fp32 sum whose last place is 1 (one rounding, to nearest even; |x * inv|
+// is at most 127 up to rounding, so nothing needs clamping).
+constexpr float kMagic = 12582912.f;
+
 __device__ __forceinline__ int quant1(float x, const Quant& q) {
-  // inv is 0 for rows that are not finite; NaN * 0 converts to 0
-  const int i = __float2int_rn(x * q.pre * q.inv);
-  return max(-127, min(127, i));
+  if (q.pre == 0.f) return 0;
+  return (int8_t)(__float_as_uint(fmaf(x * q.pre, q.inv, kMagic)) & 255u);
 }
 
-__device__ __forceinline__ uint32_t pack4(int a, int b, int c, int d) {
-  return (uint32_t)(a & 255) | ((uint32_t)(b & 255) << 8) | ((uint32_t)(c & 255) << 16) |
-         ((uint32_t)d << 24);
+// Eight of them as 8 bytes; the rare rows that are not finite or tiny take
+// the second branch together.
+__device__ __forceinline__ uint2 quant8(const float v[8], const Quant& q) {
+  uint32_t b[8];
+  if (q.pre == 1.f) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) b[i] = __float_as_uint(fmaf(v[i], q.inv, kMagic));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) b[i] = (uint32_t)quant1(v[i], q);
+  }
+  uint2 o;
+  o.x = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
+  o.y = __byte_perm(__byte_perm(b[4], b[5], 0x0040), __byte_perm(b[6], b[7], 0x0040), 0x5410);
+  return o;
+}
+
+// Bytes j .. j+7 of a row of n; vec: the row starts on an 8-byte boundary.
+__device__ __forceinline__ void row_stq(int8_t* p, int j, int n, int vec, uint2 v) {
+  if (vec && j + 8 <= n) {
+    *reinterpret_cast<uint2*>(p + j) = v;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (j + i < n) p[j + i] = (int8_t)((i < 4 ? v.x >> (8 * i) : v.y >> (8 * (i - 4))) & 255u);
+  }
 }
 
 }  // namespace ouo
