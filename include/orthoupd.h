@@ -501,7 +501,7 @@ int rms_norm_backward(const ouo_mat* dY, int dy_dtype, const ouo_mat* H,
  * the vocabulary,
  *   loss_t = tau^2 sum_k p_k (log p_k - log q_{idx_k}),
  *   lse_t  = log sum_v exp(S_tv / tau)          (for the gradient).
- * Entries whose index is outside [0, V) or whose logit is -inf do not count
+ * Entries whose index is outside [0, V) or whose logit / tau is -inf do not count
  * (padding); a row without entries has loss 0 and lse 0.  An index that
  * appears twice counts twice.  Masked student logits (-inf or the type's
  * lowest value) have q = 0: the loss is infinite (very large) where the teacher has

@@ -7,12 +7,15 @@
 //
 // HBM-bound: the loss reads the logits once (running maximum and sum), the
 // gradient reads and writes them once.
+#include <cstring>
+
 #include "tokens.cuh"
+#include "umma.cuh"
 
 namespace ouo {
 namespace {
 
-constexpr int kDThreads = 512;
+constexpr int kDThreads = 256;
 constexpr float kLowest = -3.402823466e38f;  // finite: -inf - m stays -inf
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -36,8 +39,9 @@ struct DistillArgs {
 };
 
 struct Teacher {
-  float p[OUO_DISTILL_MAX_ENTRIES];
-  int idx[OUO_DISTILL_MAX_ENTRIES];
+  float p[OUO_DISTILL_MAX_ENTRIES];    // probability
+  float lp[OUO_DISTILL_MAX_ENTRIES];   // its logarithm
+  alignas(16) int idx[OUO_DISTILL_MAX_ENTRIES];
 };
 
 __device__ __forceinline__ float block_fmax(float v, float* red) {
@@ -45,135 +49,307 @@ __device__ __forceinline__ float block_fmax(float v, float* red) {
   for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
   __syncthreads();
-  v = (threadIdx.x & 31) < (blockDim.x >> 5) ? red[threadIdx.x & 31] : kLowest;
+  v = red[0];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  for (int i = 1; i < kDThreads / 32; ++i) v = fmaxf(v, red[i]);
+  return v;
+}
+
+__device__ __forceinline__ float block_fsum(float v, float* red) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
   __syncthreads();
+  v = red[0];
+#pragma unroll
+  for (int i = 1; i < kDThreads / 32; ++i) v += red[i];
   return v;
 }
 
 // The row's teacher entries in shared memory: idx = -1 for one that does not
-// count (index outside the vocabulary, logit -inf), p its probability.
-// Returns the log of the normalizer, and through `any` whether one counts.
-__device__ __forceinline__ float teacher_probs(const DistillArgs& a, int64_t row, Teacher& t,
-                                               float* red, bool* any) {
+// count (index outside the vocabulary, logit -inf).  False if none counts.
+// red: two sets of words for the two reductions.
+__device__ __forceinline__ bool teacher_probs(const DistillArgs& a, int64_t row, Teacher& t,
+                                              float (*red)[kDThreads / 32]) {
   float m = kLowest;
   int some = 0;
-  for (int k = threadIdx.x; k < a.K; k += blockDim.x) {
+  for (int k = threadIdx.x; k < a.K; k += kDThreads) {
     int i = a.I[row * a.ldi + k];
     const float v = ld1(a.T, row * a.ldt + k, a.t_bf16) * a.inv_tau;
     if (i < 0 || i >= a.V || v == -INFINITY) i = -1;
     t.idx[k] = i;
-    t.p[k] = v;
+    t.lp[k] = v;
     if (i >= 0) {
       m = fmaxf(m, v);
       some = 1;
     }
   }
-  *any = __syncthreads_or(some) != 0;
-  m = block_fmax(m, red);
-  float z = 0.f;
-  for (int k = threadIdx.x; k < a.K; k += blockDim.x) {
-    t.p[k] -= m;
-    if (t.idx[k] >= 0) z += expf(t.p[k]);
+  if (threadIdx.x < 4) {  // whole groups of four for the search for equals
+    const int k = a.K + threadIdx.x;
+    if (k < OUO_DISTILL_MAX_ENTRIES) t.idx[k] = -1;
   }
-  z = block_sum(z, red);
-  const float lz = logf(z);
-  for (int k = threadIdx.x; k < a.K; k += blockDim.x)
-    t.p[k] = t.idx[k] >= 0 ? t.p[k] - lz : -INFINITY;  // log p
-  __syncthreads();
-  return lz;
+  if (__syncthreads_or(some) == 0) return false;
+  m = block_fmax(m, red[0]);
+  float z = 0.f;
+  for (int k = threadIdx.x; k < a.K; k += kDThreads) {
+    t.lp[k] -= m;
+    t.p[k] = t.idx[k] >= 0 ? expf(t.lp[k]) : 0.f;
+    z += t.p[k];
+  }
+  z = block_fsum(z, red[1]);
+  const float lz = logf(z), iz = 1.f / z;
+  for (int k = threadIdx.x; k < a.K; k += kDThreads) {  // the thread's own entries
+    t.lp[k] -= lz;
+    t.p[k] *= iz;
+  }
+  return true;
 }
 
-__global__ void __launch_bounds__(kDThreads) distill_kernel(const __grid_constant__ DistillArgs a) {
-  __shared__ Teacher t;
-  __shared__ float red[32];
-  __shared__ double redd[32];
-  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
-    bool any;
-    teacher_probs(a, row, t, red, &any);
-    if (!any) {
-      if (threadIdx.x == 0) {
-        a.loss[row] = 0.f;
-        a.lse[row] = 0.f;
-      }
-      __syncthreads();
-      continue;
-    }
-    // running maximum and sum of the thread's share
-    float m = kLowest, z = 0.f;
-    for (int64_t j = threadIdx.x; j < a.V; j += kDThreads) {
-      const float v = ld1(a.S, row * a.lds + j, a.s_bf16) * a.inv_tau;
-      const float mn = fmaxf(m, v);
-      z = z * ex2((m - mn) * kLog2e) + ex2((v - mn) * kLog2e);
+// A run of logits [j0, j1) of a row in 16-byte pieces: [j0, ja) and [jb, j1)
+// are taken one by one, [ja, jb) in chunks of 8 from 16-byte boundaries.
+struct Run {
+  int64_t ja, jb;
+};
+__device__ __forceinline__ Run split_run(const char* row, int es, int64_t j0, int64_t j1) {
+  const uint32_t off = (uint32_t)((uintptr_t)(row + j0 * es) & 15);
+  int64_t ja = j0 + (off ? (16 - off) / es : 0);
+  if (ja > j1) ja = j1;
+  return Run{ja, ja + (j1 - ja) / 8 * 8};
+}
+
+// Running maximum (of the raw logits) and sum of exponentials of what a
+// thread has seen; c = log2(e) / tau turns logits into exponents of two.
+struct Soft {
+  float m, z;
+  __device__ __forceinline__ void raise(float mn, float c) {
+    if (mn > m) {
+      z *= ex2((m - mn) * c);
       m = mn;
     }
-    const float M = block_fmax(m, red);
-    z = block_sum(z * ex2((m - M) * kLog2e), red);
-    const double lse = (double)M + log((double)z);
-    double acc = 0.0;
-    for (int k = threadIdx.x; k < a.K; k += kDThreads) {
-      if (t.idx[k] < 0) continue;
-      const float lp = t.p[k], p = expf(lp);
-      if (p == 0.f) continue;  // also where the student's logit is -inf
-      acc += (double)p * ((double)lp - ((double)(ld1(a.S, row * a.lds + t.idx[k], a.s_bf16) *
-                                                 a.inv_tau) - lse));
+  }
+  __device__ __forceinline__ void add1(float v, float c) {
+    raise(v, c);
+    z += ex2((v - m) * c);
+  }
+  template <int N>
+  __device__ __forceinline__ void add(const float (&v)[N], float c) {
+    float mn = v[0];
+#pragma unroll
+    for (int i = 1; i < N; ++i) mn = fmaxf(mn, v[i]);
+    raise(mn, c);
+    float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+      s0 += ex2((v[i] - m) * c);
+      s1 += ex2((v[i + 1] - m) * c);
+    }
+    z += s0 + s1;
+  }
+};
+
+// One row per cluster: its CTAs divide the vocabulary and join their maxima
+// and sums through distributed shared memory (one CTA: no join).
+template <int BF>
+__global__ void __launch_bounds__(kDThreads, 4)
+distill_kernel(const __grid_constant__ DistillArgs a) {
+  constexpr int kU = BF ? 4 : 2;  // chunks of 8 in flight per thread
+  __shared__ Teacher t;
+  __shared__ float red[4][kDThreads / 32];
+  __shared__ double redd[kDThreads / 32];
+  __shared__ float join[2];
+  uint32_t nct;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(nct));
+  const uint32_t rank = nct > 1 ? ptx::cluster_ctarank() : 0u;
+  const int64_t row = blockIdx.x / nct;
+  const bool any = teacher_probs(a, row, t, red);  // the same in every CTA of the cluster
+  if (!any) {
+    if (threadIdx.x == 0 && rank == 0) {
+      a.loss[row] = 0.f;
+      a.lse[row] = 0.f;
+    }
+    return;
+  }
+  const char* s = reinterpret_cast<const char*>(a.S) + row * a.lds * (BF ? 2 : 4);
+  const int64_t per = (a.V + nct - 1) / nct;
+  const int64_t j0 = rank * per < a.V ? rank * per : a.V;
+  const int64_t j1 = j0 + per < a.V ? j0 + per : a.V;
+  const Run r = split_run(s, BF ? 2 : 4, j0, j1);
+  const float c = a.inv_tau * kLog2e;
+  Soft f{kLowest, 0.f};
+  if (j0 + threadIdx.x < r.ja) f.add1(ld1(s, j0 + threadIdx.x, BF), c);
+  int64_t j = r.ja + 8 * threadIdx.x;
+  for (; j + 8 * kDThreads * (kU - 1) < r.jb; j += 8 * kDThreads * kU) {
+    uint4 raw[kU * (BF ? 1 : 2)];
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const uint4* p = reinterpret_cast<const uint4*>(s + (j + 8 * kDThreads * u) * (BF ? 2 : 4));
+      if (BF) {
+        raw[u] = __ldcs(p);
+      } else {
+        raw[2 * u] = __ldcs(p);
+        raw[2 * u + 1] = __ldcs(p + 1);
+      }
     }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
-    if ((threadIdx.x & 31) == 0) redd[threadIdx.x >> 5] = acc;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      for (int w = 1; w < kDThreads / 32; ++w) acc += redd[w];
-      a.loss[row] = (float)((double)a.tau * (double)a.tau * acc);
-      a.lse[row] = (float)lse;
+    for (int u = 0; u < kU; ++u) {
+      float v[8];
+      if (BF) {
+        unpack8(raw[u], v);
+      } else {
+        const uint4 x = raw[2 * u], y = raw[2 * u + 1];
+        v[0] = __uint_as_float(x.x); v[1] = __uint_as_float(x.y);
+        v[2] = __uint_as_float(x.z); v[3] = __uint_as_float(x.w);
+        v[4] = __uint_as_float(y.x); v[5] = __uint_as_float(y.y);
+        v[6] = __uint_as_float(y.z); v[7] = __uint_as_float(y.w);
+      }
+      f.add(v, c);
     }
-    __syncthreads();
+  }
+  for (; j < r.jb; j += 8 * kDThreads) {
+    float v[8];
+    ld8(s, j, BF, v);
+    f.add(v, c);
+  }
+  if (r.jb + threadIdx.x < j1) f.add1(ld1(s, r.jb + threadIdx.x, BF), c);
+
+  float M = block_fmax(f.m, red[2]);
+  float Z = block_fsum(f.z * ex2((f.m - M) * c), red[3]);
+  if (nct > 1) {
+    if (threadIdx.x == 0) {
+      join[0] = M;
+      join[1] = Z;
+    }
+    __syncwarp();
+    ptx::cluster_sync();
+    float m[8], z[8], mm = kLowest;
+#pragma unroll
+    for (int p = 0; p < 8; ++p) {
+      m[p] = kLowest;
+      z[p] = 0.f;
+      if (p < (int)nct) {
+        m[p] = ptx::ld_cluster_float(ptx::mapa(ptx::smem_u32(&join[0]), p));
+        z[p] = ptx::ld_cluster_float(ptx::mapa(ptx::smem_u32(&join[1]), p));
+      }
+      mm = fmaxf(mm, m[p]);
+    }
+    Z = 0.f;
+#pragma unroll
+    for (int p = 0; p < 8; ++p) Z += z[p] * ex2((m[p] - mm) * c);
+    M = mm;
+    __syncwarp();
+    ptx::cluster_sync();  // everyone has read everyone's
+    if (rank != 0) return;
+  }
+  // The few terms of the loss in float64: log p - log q cancels where the
+  // student is near the teacher.
+  const double lse = (double)M * (double)a.inv_tau + log((double)Z);
+  double acc = 0.0;
+  for (int k = threadIdx.x; k < a.K; k += kDThreads) {
+    const int i = t.idx[k];
+    const float p = t.p[k];
+    if (i < 0 || p == 0.f) continue;  // p = 0 also where the student's logit is -inf
+    acc += (double)p * ((double)t.lp[k] - ((double)(ld1(s, i, BF) * a.inv_tau) - lse));
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
+  if ((threadIdx.x & 31) == 0) redd[threadIdx.x >> 5] = acc;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int w = 1; w < kDThreads / 32; ++w) acc += redd[w];
+    a.loss[row] = (float)((double)a.tau * (double)a.tau * acc);
+    a.lse[row] = (float)lse;
   }
 }
 
-__global__ void __launch_bounds__(kDThreads)
-distill_bwd_kernel(const __grid_constant__ DistillArgs a) {
+// Every CTA writes one segment of one row.
+template <int BF>
+__global__ void __launch_bounds__(kDThreads, 4)
+distill_bwd_kernel(const __grid_constant__ DistillArgs a, int64_t seg, int segs) {
+  constexpr int kU = BF ? 4 : 2;
   __shared__ Teacher t;
   __shared__ float sq[OUO_DISTILL_MAX_ENTRIES];
-  __shared__ float red[32];
-  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
-    const float g = a.dloss[row] * a.tau, lse = a.lse[row];
-    bool any = false;
-    if (g != 0.f) teacher_probs(a, row, t, red, &any);
-    if (!any) {
-      for (int64_t j = threadIdx.x; j < a.V; j += kDThreads)
-        st1(a.dS, row * a.ldds + j, 0.f, a.ds_bf16);
-      __syncthreads();
-      continue;
-    }
-    auto prob = [&](int64_t j) {
-      return ex2((ld1(a.S, row * a.lds + j, a.s_bf16) * a.inv_tau - lse) * kLog2e);
-    };
+  __shared__ float red[2][kDThreads / 32];
+  const int64_t row = blockIdx.x / segs;
+  const int64_t j0 = (blockIdx.x - row * segs) * seg;
+  const int64_t j1 = j0 + seg < a.V ? j0 + seg : a.V;
+  const float g = a.dloss[row] * a.tau, lse = a.lse[row];
+  const char* s = reinterpret_cast<const char*>(a.S) + row * a.lds * (BF ? 2 : 4);
+  char* d = reinterpret_cast<char*>(a.dS) + row * a.ldds * (a.ds_bf16 ? 2 : 4);
+  const bool any = g != 0.f && teacher_probs(a, row, t, red);
+  // chunks that are 16-byte pieces of both matrices
+  Run r = split_run(s, BF ? 2 : 4, j0, j1);
+  if (((uintptr_t)d + r.ja * (a.ds_bf16 ? 2 : 4)) & 15) r.ja = r.jb = j0;
+  auto prob = [&](float x) { return ex2((x * a.inv_tau - lse) * kLog2e); };
+  if (any) {
     // dS may be S itself: the entries' own probabilities are read first
-    for (int k = threadIdx.x; k < a.K; k += kDThreads)
-      if (t.idx[k] >= 0) {
-        sq[k] = prob(t.idx[k]);
-        t.p[k] = expf(t.p[k]);
-      }
-    __syncthreads();
-    for (int64_t j = threadIdx.x; j < a.V; j += kDThreads)
-      st1(a.dS, row * a.ldds + j, g * prob(j), a.ds_bf16);
-    __syncthreads();
-    // the first entry of each index takes every entry of that index
     for (int k = threadIdx.x; k < a.K; k += kDThreads) {
       const int i = t.idx[k];
-      if (i < 0) continue;
-      float p = 0.f;
-      bool first = true;
-      for (int l = 0; l < a.K; ++l)
-        if (t.idx[l] == i) {
-          if (l < k) { first = false; break; }
-          p += t.p[l];
-        }
-      if (first) st1(a.dS, row * a.ldds + i, g * (sq[k] - p), a.ds_bf16);
+      if (i >= j0 && i < j1) sq[k] = prob(ld1(s, i, BF));
     }
     __syncthreads();
+    auto one = [&](int64_t j) { st1(d, j, g * prob(ld1(s, j, BF)), a.ds_bf16); };
+    for (int64_t j = j0 + threadIdx.x; j < r.ja; j += kDThreads) one(j);
+    for (int64_t j = r.ja + 8 * threadIdx.x; j < r.jb; j += 8 * kDThreads * kU) {
+      uint4 raw[kU * (BF ? 1 : 2)];
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        const int64_t e = j + 8 * kDThreads * u;
+        if (e >= r.jb) break;
+        const uint4* p = reinterpret_cast<const uint4*>(s + e * (BF ? 2 : 4));
+        if (BF) {
+          raw[u] = __ldcs(p);
+        } else {
+          raw[2 * u] = __ldcs(p);
+          raw[2 * u + 1] = __ldcs(p + 1);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        const int64_t e = j + 8 * kDThreads * u;
+        if (e >= r.jb) break;
+        float v[8];
+        if (BF) {
+          unpack8(raw[u], v);
+        } else {
+          const uint4 x = raw[2 * u], y = raw[2 * u + 1];
+          v[0] = __uint_as_float(x.x); v[1] = __uint_as_float(x.y);
+          v[2] = __uint_as_float(x.z); v[3] = __uint_as_float(x.w);
+          v[4] = __uint_as_float(y.x); v[5] = __uint_as_float(y.y);
+          v[6] = __uint_as_float(y.z); v[7] = __uint_as_float(y.w);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = g * prob(v[i]);
+        st8(d, e, a.ds_bf16, v);
+      }
+    }
+    for (int64_t j = r.jb + threadIdx.x; j < j1; j += kDThreads) one(j);
+    __syncthreads();
+    // the first entry of each index takes every entry of that index
+    const int4* i4 = reinterpret_cast<const int4*>(t.idx);
+    for (int k = threadIdx.x; k < a.K; k += kDThreads) {
+      const int i = t.idx[k];
+      if (i < j0 || i >= j1) continue;
+      float p = 0.f;
+      bool first = true;
+      for (int l = 0; 4 * l < a.K; ++l) {
+        const int4 x = i4[l];
+        if (x.x != i && x.y != i && x.z != i && x.w != i) continue;
+        const int e[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+          if (e[b] == i) {
+            if (4 * l + b < k) first = false;
+            p += t.p[4 * l + b];
+          }
+        if (!first) break;
+      }
+      if (first) st1(d, i, g * (sq[k] - p), a.ds_bf16);
+    }
+  } else {
+    const float zero[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    for (int64_t j = j0 + threadIdx.x; j < r.ja; j += kDThreads) st1(d, j, 0.f, a.ds_bf16);
+    for (int64_t j = r.ja + 8 * threadIdx.x; j < r.jb; j += 8 * kDThreads) st8(d, j, a.ds_bf16, zero);
+    for (int64_t j = r.jb + threadIdx.x; j < j1; j += kDThreads) st1(d, j, 0.f, a.ds_bf16);
   }
 }
 
@@ -229,8 +405,24 @@ int distill_loss(const ouo_mat* S, int s_dtype, const ouo_mat* teacher, int t_dt
   DistillArgs a = distill_args(S, s_dtype, teacher, t_dtype, idx, temperature);
   a.loss = loss;
   a.lse = lse;
-  const int64_t cap = (int64_t)num_sms() * 4;
-  distill_kernel<<<(unsigned)(a.rows < cap ? a.rows : cap), kDThreads, 0, (cudaStream_t)stream>>>(a);
+  // Few rows: a cluster per row, so that a GPU's worth of CTAs read it; a CTA
+  // keeps at least 4096 logits.
+  unsigned cluster = 1;
+  while (cluster < 8 && a.rows * cluster < 4 * num_sms() && a.V / (2 * cluster) >= 4096) cluster *= 2;
+  if (a.rows * cluster > 0x7fffffff) return set_error(OUO_ERR_UNSUPPORTED, "S: too many rows");
+  cudaLaunchConfig_t cfg;
+  memset(&cfg, 0, sizeof(cfg));
+  cfg.gridDim = dim3((unsigned)(a.rows * cluster), 1, 1);
+  cfg.blockDim = dim3(kDThreads, 1, 1);
+  cfg.stream = (cudaStream_t)stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cluster;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  OUO_CHECK_CUDA(cudaLaunchKernelEx(&cfg, a.s_bf16 ? distill_kernel<1> : distill_kernel<0>, a));
   OUO_CHECK_LAUNCH();
   return OUO_OK;
 }
@@ -255,8 +447,17 @@ int distill_loss_backward(const ouo_mat* S, int s_dtype, const ouo_mat* teacher,
   a.lse = const_cast<float*>(lse);
   a.dloss = dloss;
   a.dS = dS->ptr; a.ldds = dS->ld; a.ds_bf16 = ds_dtype == OUO_BF16;
-  const int64_t cap = (int64_t)num_sms() * 4;
-  distill_bwd_kernel<<<(unsigned)(a.rows < cap ? a.rows : cap), kDThreads, 0, (cudaStream_t)stream>>>(a);
+  // Few rows are cut into segments, of 2048 logits at least.
+  int64_t segs = ceil_div((int64_t)8 * num_sms(), a.rows);
+  if (segs > a.V / 2048) segs = a.V / 2048;
+  if (segs < 1) segs = 1;
+  const int64_t seg = ceil_div(ceil_div(a.V, segs), (int64_t)8) * 8;
+  segs = ceil_div(a.V, seg);
+  if (a.rows * segs > 0x7fffffff) return set_error(OUO_ERR_UNSUPPORTED, "S: too many rows");
+  const unsigned grid = (unsigned)(a.rows * segs);
+  cudaStream_t s = (cudaStream_t)stream;
+  if (a.s_bf16) distill_bwd_kernel<1><<<grid, kDThreads, 0, s>>>(a, seg, (int)segs);
+  else distill_bwd_kernel<0><<<grid, kDThreads, 0, s>>>(a, seg, (int)segs);
   OUO_CHECK_LAUNCH();
   return OUO_OK;
 }

@@ -195,6 +195,10 @@ __device__ __forceinline__ int ld_cluster_int(uint32_t addr) {
   return v;
 }
 
+__device__ __forceinline__ float ld_cluster_float(uint32_t addr) {
+  return __int_as_float(ld_cluster_int(addr));
+}
+
 // All threads of every CTA of the cluster.
 __device__ __forceinline__ void cluster_sync() {
   asm volatile(
