@@ -6,7 +6,10 @@
 //   dx = dh + r (w dy - h r^2 mean(w dy h)),  dw = sum over rows of dy h r
 //
 // HBM-bound: every matrix is read or written once.
+#include <mutex>
+
 #include "tokens.cuh"
+#include "umma.cuh"
 
 namespace ouo {
 namespace {
@@ -155,36 +158,94 @@ struct NormBwdArgs {
   float* part;
   int64_t rows, cols;
   int vdy, vh, vw, vdh, vdx;  // 16-byte accesses allowed
+  int depth, units;           // rows on their way; 16-byte units of a thread's chunk of one
 };
+
+__device__ __forceinline__ void copy16(void* smem, const void* g) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ptx::smem_u32(smem)), "l"(g)
+               : "memory");
+}
 
 // A block of TPR threads takes rows b, b + grid, ...; every thread keeps the
 // same columns of all of them, so that its share of dw stays in registers
-// and leaves once, to row b of the partial sums. 
+// and leaves once, to row b of the partial sums.  Where 16-byte accesses are
+// allowed, `depth` rows of dY, H and dH are on their way to shared memory
+// (cp.async, to slots that only the copying thread reads, so without
+// barriers); the reduction of a row would otherwise leave the memory idle.
 template <int TPR, int NV>
-__global__ void __launch_bounds__(TPR) rms_bwd_kernel(const __grid_constant__ NormBwdArgs a) {
+__global__ void __launch_bounds__(TPR, TPR * NV <= 512 ? 1024 / TPR : 1)
+rms_bwd_kernel(const __grid_constant__ NormBwdArgs a) {
   __shared__ float red[2][TPR / 32];
+  extern __shared__ __align__(16) uint4 ring[];
   const int t = threadIdx.x, n = (int)a.cols;
-  float w[NV][8], dw[NV][8], g[NV][8], h[NV][8];
+  float w[NV][8], dw[NV][8];
 #pragma unroll
   for (int c = 0; c < NV; ++c) {
     row_ld8(a.W, 8 * (t + c * TPR), n, a.w_bf16, a.vw, w[c]);
 #pragma unroll
     for (int i = 0; i < 8; ++i) dw[c][i] = 0.f;
   }
+  // slots of one stage, in 16-byte units a thread: dY, H, dH (fp32: two each)
+  const int u1 = a.dy_bf16 ? 1 : 2, u2 = u1 + (a.h_bf16 ? 1 : 2);
+  auto issue = [&](int64_t row, int stage) {
+    if (row < a.rows) {
+      const char* src[3] = {row_of(a.dY, row, a.lddy, a.dy_bf16), row_of(a.H, row, a.ldh, a.h_bf16),
+                            a.dH ? row_of(a.dH, row, a.lddh, a.dx_bf16) : nullptr};
+      const int bf[3] = {a.dy_bf16, a.h_bf16, a.dx_bf16}, at[3] = {0, u1, u2};
+#pragma unroll
+      for (int m = 0; m < 3; ++m) {
+        if (m == 2 && !a.dH) break;
+#pragma unroll
+        for (int c = 0; c < NV; ++c) {
+          if (8 * (t + c * TPR) >= n) break;
+          uint4* d = ring + ((stage * a.units + at[m]) * NV + c) * TPR + t;
+          const char* p = src[m] + (t + c * TPR) * (bf[m] ? 16 : 32);
+          copy16(d, p);
+          if (!bf[m]) copy16(d + NV * TPR, p + 16);
+        }
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  auto fetch = [&](RowRaw<TPR, NV>& r, int stage, int at, int bf) {
+    r.packed = bf;
+#pragma unroll
+    for (int c = 0; c < NV; ++c) {
+      const bool in = 8 * (t + c * TPR) < n;
+      const uint4* q = ring + ((stage * a.units + at) * NV + c) * TPR + t;
+      r.a[c] = in ? q[0] : make_uint4(0, 0, 0, 0);
+      if (!bf) r.b[c] = in ? q[NV * TPR] : make_uint4(0, 0, 0, 0);
+    }
+  };
+  int64_t ahead = blockIdx.x;
+  if (a.depth)
+    for (int s = 0; s < a.depth; ++s, ahead += gridDim.x) issue(ahead, s);
+  float r_next = blockIdx.x < a.rows ? a.rstd[blockIdx.x] : 0.f;
   const float inv_n = 1.f / (float)n;
-  int flip = 0;
+  int flip = 0, stage = 0;
   for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, flip ^= 1) {
-    const float r = a.rstd[row];
-    const char* dy = row_of(a.dY, row, a.lddy, a.dy_bf16);
-    const char* hp = row_of(a.H, row, a.ldh, a.h_bf16);
-    const char* dh = a.dH ? row_of(a.dH, row, a.lddh, a.dx_bf16) : nullptr;
+    const float r = r_next;
+    if (row + gridDim.x < a.rows) r_next = a.rstd[row + gridDim.x];
+    float g[NV][8], h[NV][8];
+    RowRaw<TPR, NV> dr;
+    {
+      RowRaw<TPR, NV> gr, hr;
+      if (a.depth) {
+        if (a.depth == 4) asm volatile("cp.async.wait_group 3;" ::: "memory");
+        else if (a.depth == 3) asm volatile("cp.async.wait_group 2;" ::: "memory");
+        else asm volatile("cp.async.wait_group 1;" ::: "memory");
+        fetch(gr, stage, 0, a.dy_bf16);
+        fetch(hr, stage, u1, a.h_bf16);
+        if (a.dH) fetch(dr, stage, u2, a.dx_bf16);
+      } else {
+        gr.load(row_of(a.dY, row, a.lddy, a.dy_bf16), t, n, a.dy_bf16, a.vdy);
+        hr.load(row_of(a.H, row, a.ldh, a.h_bf16), t, n, a.h_bf16, a.vh);
+        if (a.dH) dr.load(row_of(a.dH, row, a.lddh, a.dx_bf16), t, n, a.dx_bf16, a.vdh);
+      }
+      gr.get(g);
+      hr.get(h);
+    }
     float acc = 0.f;
-    RowRaw<TPR, NV> gr, hr, dr;
-    gr.load(dy, t, n, a.dy_bf16, a.vdy);
-    hr.load(hp, t, n, a.h_bf16, a.vh);
-    if (dh) dr.load(dh, t, n, a.dx_bf16, a.vdh);
-    gr.get(g);
-    hr.get(h);
 #pragma unroll
     for (int c = 0; c < NV; ++c)
 #pragma unroll
@@ -195,22 +256,28 @@ __global__ void __launch_bounds__(TPR) rms_bwd_kernel(const __grid_constant__ No
         acc = fmaf(g[c][i], h[c][i], acc);
       }
     const float m = team_sum<TPR>(acc, red[flip]) * inv_n;
-    char* dx = const_cast<char*>(row_of(a.dX, row, a.lddx, a.dx_bf16));
 #pragma unroll
     for (int c = 0; c < NV; ++c)
 #pragma unroll
       for (int i = 0; i < 8; ++i) g[c][i] = r * (g[c][i] - h[c][i] * m);
-    if (dh) {
+    if (a.dH) {
       dr.get(h);
 #pragma unroll
       for (int c = 0; c < NV; ++c)
 #pragma unroll
         for (int i = 0; i < 8; ++i) g[c][i] += h[c][i];
     }
+    if (a.depth) {  // this stage's values are in registers
+      issue(ahead, stage);
+      ahead += gridDim.x;
+      if (++stage == a.depth) stage = 0;
+    }
+    char* dx = const_cast<char*>(row_of(a.dX, row, a.lddx, a.dx_bf16));
 #pragma unroll
     for (int c = 0; c < NV; ++c)
       row_st8(dx, 8 * (t + c * TPR), n, a.dx_bf16, a.vdx, g[c]);
   }
+  if (a.depth) asm volatile("cp.async.wait_group 0;" ::: "memory");
   if (a.part) {
     float* part = a.part + blockIdx.x * a.cols;
 #pragma unroll
@@ -268,10 +335,44 @@ rms_dw_kernel(const float* part, int nparts, int64_t cols, float* dw) {
   }
 }
 
-// Rows of partial sums of dw: a function of the shape alone, so that the
-// workspace query needs no device.
-constexpr int64_t kMaxParts = 296;
-int64_t bwd_parts(int64_t rows) { return rows < kMaxParts ? rows : kMaxParts; }
+template <int TPR, int NV>
+int launch_bwd(NormBwdArgs& a, unsigned grid, cudaStream_t s) {
+  // shared memory of a block: what lets 1024 threads share an SM
+  constexpr size_t kMost = TPR * NV <= 512 ? (size_t)100 * 1024 * TPR / 512 : (size_t)200 * 1024;
+  static std::mutex mu;
+  static bool ready[64] = {false};
+  a.units = (a.dy_bf16 ? 1 : 2) + (a.h_bf16 ? 1 : 2) + (a.dH ? (a.dx_bf16 ? 1 : 2) : 0);
+  const size_t stage = (size_t)a.units * NV * TPR * 16;
+  a.depth = 0;
+  if (a.vdy && a.vh && (a.vdh || !a.dH) && a.cols % 8 == 0 && a.rows > grid) {
+    a.depth = (int)(kMost / stage);
+    if (a.depth > 4) a.depth = 4;
+    if (a.depth < 2) a.depth = 0;
+  }
+  const size_t smem = a.depth * stage;
+  if (smem > 48 * 1024) {
+    int dev = 0;
+    OUO_CHECK_CUDA(cudaGetDevice(&dev));
+    if (dev < 0 || dev >= 64)
+      return set_error(OUO_ERR_UNSUPPORTED, "device ordinal %d out of range", dev);
+    std::lock_guard<std::mutex> lock(mu);
+    if (!ready[dev]) {
+      OUO_CHECK_CUDA(cudaFuncSetAttribute(rms_bwd_kernel<TPR, NV>,
+                                          cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMost));
+      ready[dev] = true;
+    }
+  }
+  rms_bwd_kernel<TPR, NV><<<grid, TPR, smem, s>>>(a);
+  return OUO_OK;
+}
+
+// Blocks of the gradient, and rows of partial sums of dw: 1024 threads on each
+// of 148 SMs.  A function of the shape alone, so that the workspace query
+// needs no device.
+int64_t bwd_parts(int64_t rows, int64_t cols) {
+  const int64_t most = cols <= 128 * 8 ? 1184 : cols <= 512 * 8 ? 296 : 148;
+  return rows < most ? rows : most;
+}
 
 }  // namespace
 }  // namespace ouo
@@ -348,7 +449,7 @@ int rms_norm(const ouo_mat* X, int x_dtype, const ouo_mat* residual, const ouo_m
 
 size_t rms_norm_backward_workspace_bytes(int64_t rows, int64_t cols) {
   if (rows < 0 || cols < 0) return 0;
-  return (size_t)(ouo::bwd_parts(rows) * cols) * sizeof(float);
+  return (size_t)(ouo::bwd_parts(rows, cols) * cols) * sizeof(float);
 }
 
 int rms_norm_backward(const ouo_mat* dY, int dy_dtype, const ouo_mat* H, int h_dtype,
@@ -382,7 +483,7 @@ int rms_norm_backward(const ouo_mat* dY, int dy_dtype, const ouo_mat* H, int h_d
                      need, ws ? ws_bytes : (size_t)0);
   OUO_TRY(require_sm100());
   cudaStream_t s = (cudaStream_t)stream;
-  const int64_t parts = bwd_parts(T);
+  const int64_t parts = bwd_parts(T, n);
   if (T > 0) {
     NormBwdArgs a{};
     a.dY = dY->ptr; a.lddy = dY->ld; a.dy_bf16 = dy_dtype == OUO_BF16;
@@ -399,9 +500,9 @@ int rms_norm_backward(const ouo_mat* dY, int dy_dtype, const ouo_mat* H, int h_d
     a.vdh = dH ? rows16(*dH, elem_size(dx_dtype)) : 0;
     a.vdx = rows16(*dX, elem_size(dx_dtype));
     const unsigned grid = (unsigned)parts;
-    if (n <= 128 * 8) rms_bwd_kernel<128, 1><<<grid, 128, 0, s>>>(a);
-    else if (n <= 512 * 8) rms_bwd_kernel<512, 1><<<grid, 512, 0, s>>>(a);
-    else if (n <= 512 * 16) rms_bwd_kernel<512, 2><<<grid, 512, 0, s>>>(a);
+    if (n <= 128 * 8) OUO_TRY((launch_bwd<128, 1>(a, grid, s)));
+    else if (n <= 512 * 8) OUO_TRY((launch_bwd<512, 1>(a, grid, s)));
+    else if (n <= 512 * 16) OUO_TRY((launch_bwd<512, 2>(a, grid, s)));
     else rms_bwd_long_kernel<<<grid, 512, 0, s>>>(a);
     OUO_CHECK_LAUNCH();
   }

@@ -111,12 +111,11 @@ struct QuantTArgs {
   int cached;        // rows of a CTA that stay in shared memory, a multiple of 32
 };
 
-// 16 bytes of row r: columns c .. c + 16 / ES - 1, zero outside the matrix.
+// 16 bytes of row r from column c, zero outside the matrix, element by element.
 template <int BF>
 __device__ __forceinline__ uint4 seg_ld(const QuantTArgs& a, int64_t r, int64_t c) {
   constexpr int kE = BF ? 8 : 4;
   const char* p = reinterpret_cast<const char*>(a.X) + (r * a.ldx + c) * (BF ? 2 : 4);
-  if (a.vecx && c + kE <= a.cols) return *reinterpret_cast<const uint4*>(p);
   uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
   for (int i = 0; i < kE; ++i) {
@@ -160,18 +159,28 @@ quant_cols_kernel(const __grid_constant__ QuantTArgs a) {
     }
   };
   constexpr int kRowsPass = kTThreads / 4, kU = 8;
-  for (int64_t r = ra + (threadIdx.x >> 2); r < rb; r += kRowsPass * kU) {
-    uint4 u[kU];
+  const int64_t cs = c0 + seg * (BF ? 8 : 4);
+  auto keep = [&](int64_t l, const uint4& u) {
+    take(u);
+    if (l < a.cached) reinterpret_cast<uint4*>(cache)[l * 4 + seg] = u;
+  };
+  if (a.vecx && c0 + kCols <= a.cols) {
+    const char* p = reinterpret_cast<const char*>(a.X) + cs * (BF ? 2 : 4);
+    const int64_t pitch = a.ldx * (BF ? 2 : 4);
+    for (int64_t r = ra + (threadIdx.x >> 2); r < rb; r += kRowsPass * kU) {
+      uint4 u[kU];
 #pragma unroll
-    for (int k = 0; k < kU; ++k)
-      u[k] = r + k * kRowsPass < rb ? seg_ld<BF>(a, r + k * kRowsPass, c0 + seg * (16 / (BF ? 2 : 4)))
-                                    : make_uint4(0, 0, 0, 0);
+      for (int k = 0; k < kU; ++k) {
+        u[k] = make_uint4(0, 0, 0, 0);
+        if (r + k * kRowsPass < rb)
+          u[k] = *reinterpret_cast<const uint4*>(p + (r + k * kRowsPass) * pitch);
+      }
 #pragma unroll
-    for (int k = 0; k < kU; ++k) {
-      take(u[k]);
-      const int64_t l = r + k * kRowsPass - ra;
-      if (l < a.cached) reinterpret_cast<uint4*>(cache)[l * 4 + seg] = u[k];
+      for (int k = 0; k < kU; ++k)
+        if (r + k * kRowsPass < rb) keep(r + k * kRowsPass - ra, u[k]);
     }
+  } else {
+    for (int64_t r = ra + (threadIdx.x >> 2); r < rb; r += kRowsPass) keep(r - ra, seg_ld<BF>(a, r, cs));
   }
 #pragma unroll
   for (int i = 0; i < (BF ? 8 : 4); ++i) {
@@ -191,7 +200,9 @@ quant_cols_kernel(const __grid_constant__ QuantTArgs a) {
   // every thread's one or two columns: word `wd` of a row
   const int wd = lane & 15, half = lane >> 4;
   uint32_t x0 = 0, x1 = 0;
-  for (uint32_t p = 0; p < nct; ++p) {
+#pragma unroll
+  for (uint32_t p = 0; p < kMaxCluster; ++p) {
+    if (p >= nct) break;
     x0 = max(x0, (uint32_t)ptx::ld_cluster_int(
                      ptx::mapa(ptx::smem_u32(&cmax[BF ? 2 * wd : wd]), p)));
     if (BF)
@@ -211,24 +222,24 @@ quant_cols_kernel(const __grid_constant__ QuantTArgs a) {
   for (int64_t base = ra + warp * 32; base < rb; base += kTThreads) {
     const int64_t r0 = base + 16 * half;
     uint32_t w[16];
+    if (base + 32 - ra <= a.cached) {
+      const uint32_t* q = cache + (r0 - ra) * 16 + wd;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const int k = i ^ 1;  // the other half's row of this step
-      const int64_t l = r0 - ra + (half ? k : i);
-      uint32_t v = 0;
-      if (l < a.cached) {
-        v = cache[l * 16 + wd];
-      } else if (ra + l < rb) {
+      for (int i = 0; i < 16; ++i) w[i] = q[(i ^ half) * 16];
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int64_t r = r0 + (i ^ half);
+        w[i] = 0;
+        if (r >= rb) continue;
         if (BF) {
-          if (col < a.cols)
-            v = reinterpret_cast<const uint16_t*>(a.X)[(ra + l) * a.ldx + col];
-          if (col + 1 < a.cols)
-            v |= (uint32_t)reinterpret_cast<const uint16_t*>(a.X)[(ra + l) * a.ldx + col + 1] << 16;
+          const uint16_t* p = reinterpret_cast<const uint16_t*>(a.X) + r * a.ldx + col;
+          if (col < a.cols) w[i] = p[0];
+          if (col + 1 < a.cols) w[i] |= (uint32_t)p[1] << 16;
         } else if (col < a.cols) {
-          v = reinterpret_cast<const uint32_t*>(a.X)[(ra + l) * a.ldx + col];
+          w[i] = reinterpret_cast<const uint32_t*>(a.X)[r * a.ldx + col];
         }
       }
-      w[i] = v;
     }
     if (half) {
 #pragma unroll
