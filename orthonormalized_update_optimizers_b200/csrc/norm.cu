@@ -32,8 +32,9 @@ __device__ __forceinline__ const char* row_of(const void* p, int64_t r, int64_t 
 }
 
 // A team per row, h in registers (as the values that H's type holds): x and
-// the residual are read once, and nothing is read back.
-template <int TPR, int NV>
+// the residual are read once, and nothing is read back.  MODE 1 / 2: every
+// matrix and the weight bf16 / fp32, 16-byte accesses.
+template <int TPR, int NV, int MODE>
 __global__ void __launch_bounds__(kTeamThreads<TPR>) rms_kernel(const __grid_constant__ NormArgs a) {
   constexpr int kWarps = kTeamThreads<TPR> / 32, kTeams = kTeamThreads<TPR> / TPR;
   __shared__ float reds[kWarps];
@@ -41,26 +42,40 @@ __global__ void __launch_bounds__(kTeamThreads<TPR>) rms_kernel(const __grid_con
   const int64_t row = (int64_t)blockIdx.x * kTeams + (kTeams > 1 ? threadIdx.x / TPR : 0);
   if (kTeams > 1 && row >= a.rows) return;
   const int t = threadIdx.x % TPR, n = (int)a.cols;
-  RowRaw<TPR, NV> xr, rr;
+  const int xb = MODE ? MODE == 1 : a.x_bf16, hb = MODE ? MODE == 1 : a.h_bf16;
+  const int wb = MODE ? MODE == 1 : a.w_bf16, yb = MODE ? MODE == 1 : a.y_bf16;
+  RowRaw<TPR, NV, MODE> xr, rr;
   float v[NV][8];
-  xr.load(row_of(a.X, row, a.ldx, a.x_bf16), t, n, a.x_bf16, a.vx);
-  if (a.R) rr.load(row_of(a.R, row, a.ldr, a.h_bf16), t, n, a.h_bf16, a.vr);
-  xr.get(v);
+  xr.load(row_of(a.X, row, a.ldx, xb), t, n, xb, a.vx);
   if (a.R) {
+    rr.load(row_of(a.R, row, a.ldr, hb), t, n, hb, a.vr);
+    xr.get(v);
     float u[NV][8];
     rr.get(u);
 #pragma unroll
     for (int c = 0; c < NV; ++c)
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[c][i] += u[c][i];
+  } else {
+    xr.get(v);
   }
   if (a.H) {
-    char* h = const_cast<char*>(row_of(a.H, row, a.ldh, a.h_bf16));
+    char* h = const_cast<char*>(row_of(a.H, row, a.ldh, hb));
+    if (MODE == 1) {
 #pragma unroll
-    for (int c = 0; c < NV; ++c) {
-      row_st8(h, 8 * (t + c * TPR), n, a.h_bf16, a.vh, v[c]);
+      for (int c = 0; c < NV; ++c) {
+        const uint4 u = pack8(v[c]);
+        if (8 * (t + c * TPR) < n) reinterpret_cast<uint4*>(h)[t + c * TPR] = u;
+        unpack8(u, v[c]);
+      }
+    } else {
+      store_row<TPR, NV, MODE>(h, t, n, hb, a.vh, v);
+      if (MODE == 0) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[c][i] = round_to(v[c][i], a.h_bf16);
+        for (int c = 0; c < NV; ++c)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[c][i] = round_to(v[c][i], hb);
+      }
     }
   }
   float acc = 0.f;
@@ -68,26 +83,27 @@ __global__ void __launch_bounds__(kTeamThreads<TPR>) rms_kernel(const __grid_con
   for (int c = 0; c < NV; ++c)
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc = fmaf(v[c][i], v[c][i], acc);
+  // the weight is on its way while the squares are summed
+  RowRaw<TPR, NV, MODE> wr;
+  wr.load(a.W, t, n, wb, a.vw);
   const float rstd = __frsqrt_rn(team_sum<TPR>(acc, reds) / (float)n + a.eps);
   if (a.rstd && t == 0) a.rstd[row] = rstd;
-  uint32_t m = 0;
+  float m = 0.f;
+  {
+    float w[NV][8];
+    wr.get(w);
 #pragma unroll
-  for (int c = 0; c < NV; ++c) {
-    float w[8];
-    row_ld8(a.W, 8 * (t + c * TPR), n, a.w_bf16, a.vw, w);
+    for (int c = 0; c < NV; ++c)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      v[c][i] = v[c][i] * rstd * w[i];
-      m = max(m, mag(v[c][i]));
-    }
+      for (int i = 0; i < 8; ++i) {
+        v[c][i] = v[c][i] * rstd * w[c][i];
+        m = max_mag(m, v[c][i]);
+      }
   }
-  if (a.Y) {
-    char* y = const_cast<char*>(row_of(a.Y, row, a.ldy, a.y_bf16));
-#pragma unroll
-    for (int c = 0; c < NV; ++c) row_st8(y, 8 * (t + c * TPR), n, a.y_bf16, a.vy, v[c]);
-  }
+  if (a.Y)
+    store_row<TPR, NV, MODE>(const_cast<char*>(row_of(a.Y, row, a.ldy, yb)), t, n, yb, a.vy, v);
   if (!a.Q) return;
-  const Quant q = quant_of(team_max<TPR>(m, redm));
+  const Quant q = quant_of(team_max<TPR>(__float_as_uint(m), redm));
   if (t == 0) a.scale[row] = q.scale;
 #pragma unroll
   for (int c = 0; c < NV; ++c)
@@ -129,17 +145,17 @@ __global__ void __launch_bounds__(512) rms_long_kernel(const __grid_constant__ N
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = v[i] * rstd * w[i];
   };
-  uint32_t m = 0;
+  float m = 0.f;
   for (int j = 8 * threadIdx.x; j < n; j += 8 * 512) {
     float v[8];
     value(j, v);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, mag(v[i]));
+    for (int i = 0; i < 8; ++i) m = max_mag(m, v[i]);
     if (a.Y)
       row_st8(const_cast<char*>(row_of(a.Y, row, a.ldy, a.y_bf16)), j, n, a.y_bf16, a.vy, v);
   }
   if (!a.Q) return;
-  const Quant q = quant_of(block_max(m, red));
+  const Quant q = quant_of(block_max(__float_as_uint(m), red));
   if (threadIdx.x == 0) a.scale[row] = q.scale;
   for (int j = 8 * threadIdx.x; j < n; j += 8 * 512) {
     float v[8];
@@ -158,26 +174,23 @@ struct NormBwdArgs {
   float* part;
   int64_t rows, cols;
   int vdy, vh, vw, vdh, vdx;  // 16-byte accesses allowed
-  int depth, units;           // rows on their way; 16-byte units of a thread's chunk of one
 };
-
-__device__ __forceinline__ void copy16(void* smem, const void* g) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ptx::smem_u32(smem)), "l"(g)
-               : "memory");
-}
 
 // A block of TPR threads takes rows b, b + grid, ...; every thread keeps the
 // same columns of all of them, so that its share of dw stays in registers
-// and leaves once, to row b of the partial sums.  Where 16-byte accesses are
-// allowed, `depth` rows of dY, H and dH are on their way to shared memory
-// (cp.async, to slots that only the copying thread reads, so without
-// barriers); the reduction of a row would otherwise leave the memory idle.
-template <int TPR, int NV>
-__global__ void __launch_bounds__(TPR, TPR * NV <= 512 ? 1024 / TPR : 1)
-rms_bwd_kernel(const __grid_constant__ NormBwdArgs a) {
+// and leaves once, to row b of the partial sums.  MODE 1 / 2 (every matrix
+// bf16 / fp32, 16-byte accesses): DEPTH rows of dY, H and dH are on their way
+// to shared memory (cp.async, to slots that only the copying thread reads, so
+// without barriers), since the reduction of a row would otherwise leave the
+// memory idle.
+template <int TPR, int NV, int MODE, int DEPTH>
+__global__ void __launch_bounds__(TPR) rms_bwd_kernel(const __grid_constant__ NormBwdArgs a) {
   __shared__ float red[2][TPR / 32];
-  extern __shared__ __align__(16) uint4 ring[];
+  extern __shared__ __align__(16) uint4 ring[];  // [DEPTH][3][NV][kUnits][TPR]
+  constexpr int kUnits = MODE == 2 ? 2 : 1;      // 16-byte pieces of a chunk
   const int t = threadIdx.x, n = (int)a.cols;
+  const int dyb = MODE ? MODE == 1 : a.dy_bf16, hb = MODE ? MODE == 1 : a.h_bf16;
+  const int dxb = MODE ? MODE == 1 : a.dx_bf16;
   float w[NV][8], dw[NV][8];
 #pragma unroll
   for (int c = 0; c < NV; ++c) {
@@ -185,62 +198,63 @@ rms_bwd_kernel(const __grid_constant__ NormBwdArgs a) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) dw[c][i] = 0.f;
   }
-  // slots of one stage, in 16-byte units a thread: dY, H, dH (fp32: two each)
-  const int u1 = a.dy_bf16 ? 1 : 2, u2 = u1 + (a.h_bf16 ? 1 : 2);
+  const char* src[3] = {row_of(a.dY, blockIdx.x, a.lddy, dyb), row_of(a.H, blockIdx.x, a.ldh, hb),
+                        a.dH ? row_of(a.dH, blockIdx.x, a.lddh, dxb) : nullptr};
+  const int64_t step[3] = {a.lddy * (dyb ? 2 : 4) * gridDim.x, a.ldh * (hb ? 2 : 4) * gridDim.x,
+                           a.lddh * (dxb ? 2 : 4) * gridDim.x};
   auto issue = [&](int64_t row, int stage) {
     if (row < a.rows) {
-      const char* src[3] = {row_of(a.dY, row, a.lddy, a.dy_bf16), row_of(a.H, row, a.ldh, a.h_bf16),
-                            a.dH ? row_of(a.dH, row, a.lddh, a.dx_bf16) : nullptr};
-      const int bf[3] = {a.dy_bf16, a.h_bf16, a.dx_bf16}, at[3] = {0, u1, u2};
 #pragma unroll
       for (int m = 0; m < 3; ++m) {
         if (m == 2 && !a.dH) break;
 #pragma unroll
         for (int c = 0; c < NV; ++c) {
           if (8 * (t + c * TPR) >= n) break;
-          uint4* d = ring + ((stage * a.units + at[m]) * NV + c) * TPR + t;
-          const char* p = src[m] + (t + c * TPR) * (bf[m] ? 16 : 32);
-          copy16(d, p);
-          if (!bf[m]) copy16(d + NV * TPR, p + 16);
+#pragma unroll
+          for (int u = 0; u < kUnits; ++u)
+            ptx::copy16(ring + (((stage * 3 + m) * NV + c) * kUnits + u) * TPR + t,
+                        src[m] + ((t + c * TPR) * kUnits + u) * 16);
         }
+        src[m] += step[m];
       }
     }
-    asm volatile("cp.async.commit_group;" ::: "memory");
+    ptx::copy16_commit();
   };
-  auto fetch = [&](RowRaw<TPR, NV>& r, int stage, int at, int bf) {
-    r.packed = bf;
+  auto fetch = [&](RowRaw<TPR, NV, MODE>& r, int stage, int m) {
 #pragma unroll
     for (int c = 0; c < NV; ++c) {
       const bool in = 8 * (t + c * TPR) < n;
-      const uint4* q = ring + ((stage * a.units + at) * NV + c) * TPR + t;
+      const uint4* q = ring + ((stage * 3 + m) * NV + c) * kUnits * TPR + t;
       r.a[c] = in ? q[0] : make_uint4(0, 0, 0, 0);
-      if (!bf) r.b[c] = in ? q[NV * TPR] : make_uint4(0, 0, 0, 0);
+      if (MODE != 1) r.b[MODE == 1 ? 0 : c] = in ? q[(kUnits - 1) * TPR] : make_uint4(0, 0, 0, 0);
     }
   };
   int64_t ahead = blockIdx.x;
-  if (a.depth)
-    for (int s = 0; s < a.depth; ++s, ahead += gridDim.x) issue(ahead, s);
+  if (MODE) {
+#pragma unroll
+    for (int s = 0; s < DEPTH; ++s, ahead += gridDim.x) issue(ahead, s);
+  }
   float r_next = blockIdx.x < a.rows ? a.rstd[blockIdx.x] : 0.f;
   const float inv_n = 1.f / (float)n;
+  char* dx = const_cast<char*>(row_of(a.dX, blockIdx.x, a.lddx, dxb));
+  const int64_t dx_step = a.lddx * (dxb ? 2 : 4) * gridDim.x;
   int flip = 0, stage = 0;
-  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, flip ^= 1) {
+  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, flip ^= 1, dx += dx_step) {
     const float r = r_next;
     if (row + gridDim.x < a.rows) r_next = a.rstd[row + gridDim.x];
     float g[NV][8], h[NV][8];
-    RowRaw<TPR, NV> dr;
+    RowRaw<TPR, NV, MODE> dr;
     {
-      RowRaw<TPR, NV> gr, hr;
-      if (a.depth) {
-        if (a.depth == 4) asm volatile("cp.async.wait_group 3;" ::: "memory");
-        else if (a.depth == 3) asm volatile("cp.async.wait_group 2;" ::: "memory");
-        else asm volatile("cp.async.wait_group 1;" ::: "memory");
-        fetch(gr, stage, 0, a.dy_bf16);
-        fetch(hr, stage, u1, a.h_bf16);
-        if (a.dH) fetch(dr, stage, u2, a.dx_bf16);
+      RowRaw<TPR, NV, MODE> gr, hr;
+      if (MODE) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 1) : "memory");
+        fetch(gr, stage, 0);
+        fetch(hr, stage, 1);
+        if (a.dH) fetch(dr, stage, 2);
       } else {
-        gr.load(row_of(a.dY, row, a.lddy, a.dy_bf16), t, n, a.dy_bf16, a.vdy);
-        hr.load(row_of(a.H, row, a.ldh, a.h_bf16), t, n, a.h_bf16, a.vh);
-        if (a.dH) dr.load(row_of(a.dH, row, a.lddh, a.dx_bf16), t, n, a.dx_bf16, a.vdh);
+        gr.load(row_of(a.dY, row, a.lddy, dyb), t, n, dyb, a.vdy);
+        hr.load(row_of(a.H, row, a.ldh, hb), t, n, hb, a.vh);
+        if (a.dH) dr.load(row_of(a.dH, row, a.lddh, dxb), t, n, dxb, a.vdh);
       }
       gr.get(g);
       hr.get(h);
@@ -255,11 +269,12 @@ rms_bwd_kernel(const __grid_constant__ NormBwdArgs a) {
         g[c][i] *= w[c][i];
         acc = fmaf(g[c][i], h[c][i], acc);
       }
-    const float m = team_sum<TPR>(acc, red[flip]) * inv_n;
+    // r (g - h m) + dh, with r m once per row
+    const float rm = team_sum<TPR>(acc, red[flip]) * inv_n * r;
 #pragma unroll
     for (int c = 0; c < NV; ++c)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) g[c][i] = r * (g[c][i] - h[c][i] * m);
+      for (int i = 0; i < 8; ++i) g[c][i] = fmaf(g[c][i], r, -(h[c][i] * rm));
     if (a.dH) {
       dr.get(h);
 #pragma unroll
@@ -267,17 +282,14 @@ rms_bwd_kernel(const __grid_constant__ NormBwdArgs a) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) g[c][i] += h[c][i];
     }
-    if (a.depth) {  // this stage's values are in registers
+    if (MODE) {  // this stage's values are in registers
       issue(ahead, stage);
       ahead += gridDim.x;
-      if (++stage == a.depth) stage = 0;
+      if (++stage == DEPTH) stage = 0;
     }
-    char* dx = const_cast<char*>(row_of(a.dX, row, a.lddx, a.dx_bf16));
-#pragma unroll
-    for (int c = 0; c < NV; ++c)
-      row_st8(dx, 8 * (t + c * TPR), n, a.dx_bf16, a.vdx, g[c]);
+    store_row<TPR, NV, MODE>(dx, t, n, dxb, a.vdx, g);
   }
-  if (a.depth) asm volatile("cp.async.wait_group 0;" ::: "memory");
+  if (MODE) ptx::copy16_wait_all();
   if (a.part) {
     float* part = a.part + blockIdx.x * a.cols;
 #pragma unroll
@@ -335,42 +347,42 @@ rms_dw_kernel(const float* part, int nparts, int64_t cols, float* dw) {
   }
 }
 
-template <int TPR, int NV>
-int launch_bwd(NormBwdArgs& a, unsigned grid, cudaStream_t s) {
-  // shared memory of a block: what lets 1024 threads share an SM
-  constexpr size_t kMost = TPR * NV <= 512 ? (size_t)100 * 1024 * TPR / 512 : (size_t)200 * 1024;
-  static std::mutex mu;
-  static bool ready[64] = {false};
-  a.units = (a.dy_bf16 ? 1 : 2) + (a.h_bf16 ? 1 : 2) + (a.dH ? (a.dx_bf16 ? 1 : 2) : 0);
-  const size_t stage = (size_t)a.units * NV * TPR * 16;
-  a.depth = 0;
-  if (a.vdy && a.vh && (a.vdh || !a.dH) && a.cols % 8 == 0 && a.rows > grid) {
-    a.depth = (int)(kMost / stage);
-    if (a.depth > 4) a.depth = 4;
-    if (a.depth < 2) a.depth = 0;
-  }
-  const size_t smem = a.depth * stage;
-  if (smem > 48 * 1024) {
+template <int TPR, int NV, int MODE, int DEPTH>
+int launch_bwd_as(const NormBwdArgs& a, unsigned grid, cudaStream_t s) {
+  constexpr size_t kSmem = MODE ? (size_t)DEPTH * 3 * NV * TPR * 16 * (MODE == 2 ? 2 : 1) : 0;
+  if (kSmem > 40 * 1024) {  // with the static part, past the default limit
+    static std::mutex mu;
+    static bool ready[64] = {false};
     int dev = 0;
     OUO_CHECK_CUDA(cudaGetDevice(&dev));
     if (dev < 0 || dev >= 64)
       return set_error(OUO_ERR_UNSUPPORTED, "device ordinal %d out of range", dev);
     std::lock_guard<std::mutex> lock(mu);
     if (!ready[dev]) {
-      OUO_CHECK_CUDA(cudaFuncSetAttribute(rms_bwd_kernel<TPR, NV>,
-                                          cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMost));
+      OUO_CHECK_CUDA(cudaFuncSetAttribute(rms_bwd_kernel<TPR, NV, MODE, DEPTH>,
+                                          cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem));
       ready[dev] = true;
     }
   }
-  rms_bwd_kernel<TPR, NV><<<grid, TPR, smem, s>>>(a);
+  rms_bwd_kernel<TPR, NV, MODE, DEPTH><<<grid, TPR, kSmem, s>>>(a);
+  OUO_CHECK_LAUNCH();
   return OUO_OK;
 }
 
-// Blocks of the gradient, and rows of partial sums of dw: 1024 threads on each
-// of 148 SMs.  A function of the shape alone, so that the workspace query
-// needs no device.
+template <int TPR, int NV>
+int launch_bwd(const NormBwdArgs& a, unsigned grid, cudaStream_t s) {
+  const bool vec = a.vdy && a.vh && a.vdx && (a.vdh || !a.dH) && a.cols % 8 == 0;
+  const int bf = a.dy_bf16 + a.h_bf16 + a.dx_bf16;
+  if (vec && bf == 3) return launch_bwd_as<TPR, NV, 1, 4>(a, grid, s);
+  if (vec && bf == 0) return launch_bwd_as<TPR, NV, 2, 2>(a, grid, s);
+  return launch_bwd_as<TPR, NV, 0, 1>(a, grid, s);
+}
+
+// Blocks of the gradient, and rows of partial sums of dw: what 148 SMs hold
+// at once.  A function of the shape alone, so that the workspace query needs
+// no device.
 int64_t bwd_parts(int64_t rows, int64_t cols) {
-  const int64_t most = cols <= 128 * 8 ? 1184 : cols <= 512 * 8 ? 296 : 148;
+  const int64_t most = 148 * (cols <= 128 * 8 ? 7 : cols <= 128 * 16 ? 4 : cols <= 256 * 16 ? 2 : 1);
   return rows < most ? rows : most;
 }
 
@@ -438,10 +450,17 @@ int rms_norm(const ouo_mat* X, int x_dtype, const ouo_mat* residual, const ouo_m
     OUO_CHECK_LAUNCH();
     return OUO_OK;
   }
-  return with_team(t, [&](auto tpr, auto nv) -> int {
+  // one type throughout, and 16-byte accesses to all of it
+  const bool vec = a.vx && a.vw && (!a.R || a.vr) && (!a.H || a.vh) && (!a.Y || a.vy) && n % 8 == 0;
+  auto all = [&](int dt) {
+    return vec && x_dtype == dt && w_dtype == dt && (!H || h_dtype == dt) && (!Y || y_dtype == dt);
+  };
+  const int fast = all(OUO_BF16) ? 1 : all(OUO_F32) ? 2 : 0;
+  return with_team(t, fast, [&](auto tpr, auto nv, auto mode) -> int {
     constexpr int TPR = decltype(tpr)::value, NV = decltype(nv)::value;
+    constexpr int MODE = decltype(mode)::value;
     constexpr int kTeams = kTeamThreads<TPR> / TPR;
-    rms_kernel<TPR, NV><<<(unsigned)ceil_div(T, (int64_t)kTeams), kTeamThreads<TPR>, 0, s>>>(a);
+    rms_kernel<TPR, NV, MODE><<<(unsigned)ceil_div(T, (int64_t)kTeams), kTeamThreads<TPR>, 0, s>>>(a);
     OUO_CHECK_LAUNCH();
     return OUO_OK;
   });
@@ -501,10 +520,13 @@ int rms_norm_backward(const ouo_mat* dY, int dy_dtype, const ouo_mat* H, int h_d
     a.vdx = rows16(*dX, elem_size(dx_dtype));
     const unsigned grid = (unsigned)parts;
     if (n <= 128 * 8) OUO_TRY((launch_bwd<128, 1>(a, grid, s)));
-    else if (n <= 512 * 8) OUO_TRY((launch_bwd<512, 1>(a, grid, s)));
+    else if (n <= 128 * 16) OUO_TRY((launch_bwd<128, 2>(a, grid, s)));
+    else if (n <= 256 * 16) OUO_TRY((launch_bwd<256, 2>(a, grid, s)));
     else if (n <= 512 * 16) OUO_TRY((launch_bwd<512, 2>(a, grid, s)));
-    else rms_bwd_long_kernel<<<grid, 512, 0, s>>>(a);
-    OUO_CHECK_LAUNCH();
+    else {
+      rms_bwd_long_kernel<<<grid, 512, 0, s>>>(a);
+      OUO_CHECK_LAUNCH();
+    }
   }
   if (dweight && n > 0) {
     rms_dw_kernel<<<(unsigned)ceil_div(n, 32), 512, 0, s>>>((const float*)ws, (int)parts, n,

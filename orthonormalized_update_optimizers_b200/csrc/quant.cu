@@ -36,7 +36,7 @@ __device__ __forceinline__ int matrix_of(const QuantArgs& a, int64_t row) {
 }
 
 // A team per row, the row in registers: one read, one write.
-template <int TPR, int NV>
+template <int TPR, int NV, int MODE>
 __global__ void __launch_bounds__(kTeamThreads<TPR>)
 quant_rows_kernel(const __grid_constant__ QuantArgs a) {
   __shared__ uint32_t red[kTeamThreads<TPR> / 32];
@@ -48,16 +48,16 @@ quant_rows_kernel(const __grid_constant__ QuantArgs a) {
   const int64_t r = row - a.row_start[g];
   const int n = (int)a.cols[g];
   const char* x = reinterpret_cast<const char*>(a.X[g]) + r * a.ldx[g] * (a.bf16 ? 2 : 4);
-  RowRaw<TPR, NV> raw;
+  RowRaw<TPR, NV, MODE> raw;
   float v[NV][8];
   raw.load(x, t, n, a.bf16, a.vecx[g]);
   raw.get(v);
-  uint32_t m = 0;
+  float m = 0.f;
 #pragma unroll
   for (int c = 0; c < NV; ++c)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, mag(v[c][i]));
-  const Quant q = quant_of(team_max<TPR>(m, red));
+    for (int i = 0; i < 8; ++i) m = max_mag(m, v[c][i]);
+  const Quant q = quant_of(team_max<TPR>(__float_as_uint(m), red));
   if (t == 0) a.scale[g][r] = q.scale;
   int8_t* o = a.Q[g] + r * a.ldq[g];
 #pragma unroll
@@ -74,14 +74,14 @@ __global__ void __launch_bounds__(512) quant_long_kernel(const __grid_constant__
   const int64_t n = a.cols[g];
   const char* x = reinterpret_cast<const char*>(a.X[g]) + r * a.ldx[g] * (a.bf16 ? 2 : 4);
   int8_t* o = a.Q[g] + r * a.ldq[g];
-  uint32_t m = 0;
+  float m = 0.f;
   for (int64_t j = 8 * threadIdx.x; j < n; j += 8 * 512) {
     float v[8];
     row_ld8(x, (int)j, (int)n, a.bf16, a.vecx[g], v);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, mag(v[i]));
+    for (int i = 0; i < 8; ++i) m = max_mag(m, v[i]);
   }
-  const Quant q = quant_of(block_max(m, red));
+  const Quant q = quant_of(block_max(__float_as_uint(m), red));
   if (threadIdx.x == 0) a.scale[g][r] = q.scale;
   for (int64_t j = 8 * threadIdx.x; j < n; j += 8 * 512) {
     float v[8];
@@ -127,7 +127,7 @@ __device__ __forceinline__ uint4 seg_ld(const QuantTArgs& a, int64_t r, int64_t 
 }
 
 template <int BF>
-__global__ void __launch_bounds__(kTThreads)
+__global__ void __launch_bounds__(kTThreads, 3)
 quant_cols_kernel(const __grid_constant__ QuantTArgs a) {
   constexpr int kCols = BF ? 32 : 16;  // of the strip
   extern __shared__ __align__(16) uint32_t cache[];  // [cached][16 words]
@@ -158,16 +158,26 @@ quant_cols_kernel(const __grid_constant__ QuantTArgs a) {
       }
     }
   };
-  constexpr int kRowsPass = kTThreads / 4, kU = 8;
+  constexpr int kRowsPass = kTThreads / 4;
   const int64_t cs = c0 + seg * (BF ? 8 : 4);
   auto keep = [&](int64_t l, const uint4& u) {
     take(u);
     if (l < a.cached) reinterpret_cast<uint4*>(cache)[l * 4 + seg] = u;
   };
   if (a.vecx && c0 + kCols <= a.cols) {
+    // every row that stays is requested at once; the thread that copied a
+    // piece is the one that looks at it
     const char* p = reinterpret_cast<const char*>(a.X) + cs * (BF ? 2 : 4);
     const int64_t pitch = a.ldx * (BF ? 2 : 4);
-    for (int64_t r = ra + (threadIdx.x >> 2); r < rb; r += kRowsPass * kU) {
+    const int lt = threadIdx.x >> 2;
+    const int ln = rb > ra ? (int)(rb - ra < a.cached ? rb - ra : a.cached) : 0;
+    for (int l = lt; l < ln; l += kRowsPass)
+      ptx::copy16(cache + l * 16 + seg * 4, p + (ra + l) * pitch);
+    ptx::copy16_wait_all();
+#pragma unroll 4
+    for (int l = lt; l < ln; l += kRowsPass) take(reinterpret_cast<const uint4*>(cache)[l * 4 + seg]);
+    constexpr int kU = 4;
+    for (int64_t r = ra + ln + lt; r < rb; r += kRowsPass * kU) {
       uint4 u[kU];
 #pragma unroll
       for (int k = 0; k < kU; ++k) {
@@ -176,8 +186,7 @@ quant_cols_kernel(const __grid_constant__ QuantTArgs a) {
           u[k] = *reinterpret_cast<const uint4*>(p + (r + k * kRowsPass) * pitch);
       }
 #pragma unroll
-      for (int k = 0; k < kU; ++k)
-        if (r + k * kRowsPass < rb) keep(r + k * kRowsPass - ra, u[k]);
+      for (int k = 0; k < kU; ++k) take(u[k]);
     }
   } else {
     for (int64_t r = ra + (threadIdx.x >> 2); r < rb; r += kRowsPass) keep(r - ra, seg_ld<BF>(a, r, cs));
@@ -374,16 +383,20 @@ extern "C" int quantize_int8(const ouo_mat* X, int x_dtype, const ouo_mat* Q, fl
     a.row_start[cn] = acc;
     if (acc == 0) continue;
     if (acc > 0x7fffffff) return set_error(OUO_ERR_UNSUPPORTED, "X: too many rows in one batch");
+    int fast = bf16 ? 1 : 2;
+    for (int i = 0; i < cn; ++i)
+      if (!a.vecx[i] || a.cols[i] % 8 != 0) fast = 0;
     const Team t = team_for(acc, longest);
     if (t.tpr == 0) {
       quant_long_kernel<<<(unsigned)acc, 512, 0, s>>>(a);
       OUO_CHECK_LAUNCH();
       continue;
     }
-    OUO_TRY(with_team(t, [&](auto tpr, auto nv) -> int {
+    OUO_TRY(with_team(t, fast, [&](auto tpr, auto nv, auto mode) -> int {
       constexpr int TPR = decltype(tpr)::value, NV = decltype(nv)::value;
+      constexpr int MODE = decltype(mode)::value;
       constexpr int kTeams = kTeamThreads<TPR> / TPR;
-      quant_rows_kernel<TPR, NV><<<(unsigned)ceil_div(acc, (int64_t)kTeams), kTeamThreads<TPR>, 0, s>>>(a);
+      quant_rows_kernel<TPR, NV, MODE><<<(unsigned)ceil_div(acc, (int64_t)kTeams), kTeamThreads<TPR>, 0, s>>>(a);
       OUO_CHECK_LAUNCH();
       return OUO_OK;
     }));

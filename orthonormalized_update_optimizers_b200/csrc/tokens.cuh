@@ -70,6 +70,15 @@ __device__ __forceinline__ void unpack8(const uint4& u, float v[8]) {
   }
 }
 
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+__device__ __forceinline__ uint4 pack8(const float v[8]) {
+  return make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7]));
+}
+
 // Elements i .. i+7 (p + i on a 16-byte boundary).
 __device__ __forceinline__ void ld8(const void* p, int64_t i, int bf16, float v[8]) {
   if (bf16) {
@@ -84,12 +93,7 @@ __device__ __forceinline__ void ld8(const void* p, int64_t i, int bf16, float v[
 
 __device__ __forceinline__ void st8(void* p, int64_t i, int bf16, const float v[8]) {
   if (bf16) {
-    uint4 u;
-    u.x = pack_bf16x2(v[0], v[1]);
-    u.y = pack_bf16x2(v[2], v[3]);
-    u.z = pack_bf16x2(v[4], v[5]);
-    u.w = pack_bf16x2(v[6], v[7]);
-    *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p) + i) = u;
+    *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p) + i) = pack8(v);
   } else {
     float4* q = reinterpret_cast<float4*>(reinterpret_cast<float*>(p) + i);
     q[0] = make_float4(v[0], v[1], v[2], v[3]);
@@ -101,9 +105,11 @@ __device__ __forceinline__ float round_to(float v, int bf16) {
   return bf16 ? bf16_to_f32(f32_to_bf16(v)) : v;
 }
 
-// The larger of two magnitudes, NaN if either is: the bit patterns of
-// non-negative floats order as integers, with NaN above infinity.
-__device__ __forceinline__ uint32_t mag(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+// The larger of m and |v|, NaN if either is NaN.
+__device__ __forceinline__ float max_mag(float m, float v) {
+  asm("max.NaN.f32 %0, %0, %1;" : "+f"(m) : "f"(fabsf(v)));
+  return m;
+}
 
 // Sum / maximum over a block of at most 1024 threads; every thread gets the
 // result.  `red` holds 32 words of shared memory and is free again on return.
@@ -188,60 +194,66 @@ __device__ __forceinline__ void row_st8(void* p, int j, int n, int bf16, int vec
 }
 
 // A thread's chunks of one row, as they are stored.  Loading and converting
-// are separate, and each branches once on the element type: every load of the
-// row is in flight before the first one is waited for.
-template <int TPR, int NV>
+// are separate, so that every load of the row is in flight before the first
+// one is waited for.  MODE 1: bf16, 2: fp32, both with 16-byte accesses and n
+// a multiple of 8, known when the kernel is compiled; 0: any type, alignment
+// and n (element by element, kept as fp32).
+template <int TPR, int NV, int MODE>
 struct RowRaw {
-  uint4 a[NV], b[NV];  // b: the second half of fp32 chunks
-  int packed;          // a holds 8 bf16 (else a, b hold 8 fp32)
+  uint4 a[NV], b[MODE == 1 ? 1 : NV];  // b: the second half of fp32 chunks
 
-  // fast: 16-byte accesses allowed and n a multiple of 8
+  __device__ __forceinline__ void set(int c, const float v[8]) {
+    a[c] = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                      __float_as_uint(v[3]));
+    b[MODE == 1 ? 0 : c] = make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]),
+                                      __float_as_uint(v[6]), __float_as_uint(v[7]));
+  }
+
   __device__ __forceinline__ void load(const void* p, int t, int n, int bf16, int vec) {
     const uint4 zero = make_uint4(0, 0, 0, 0);
-    if (vec && (n & 7) == 0) {
-      packed = bf16;
-      if (bf16) {
-        const uint4* q = reinterpret_cast<const uint4*>(p);
+    const uint4* q = reinterpret_cast<const uint4*>(p);
 #pragma unroll
-        for (int c = 0; c < NV; ++c) a[c] = 8 * (t + c * TPR) < n ? q[t + c * TPR] : zero;
+    for (int c = 0; c < NV; ++c) {
+      const int i = t + c * TPR;
+      if (MODE == 1) {
+        a[c] = 8 * i < n ? q[i] : zero;
+      } else if (MODE == 2) {
+        a[c] = 8 * i < n ? q[2 * i] : zero;
+        b[c] = 8 * i < n ? q[2 * i + 1] : zero;
       } else {
-        const uint4* q = reinterpret_cast<const uint4*>(p);
-#pragma unroll
-        for (int c = 0; c < NV; ++c) {
-          const bool in = 8 * (t + c * TPR) < n;
-          a[c] = in ? q[2 * (t + c * TPR)] : zero;
-          b[c] = in ? q[2 * (t + c * TPR) + 1] : zero;
-        }
-      }
-    } else {
-      packed = 0;
-#pragma unroll
-      for (int c = 0; c < NV; ++c) {
         float v[8];
-        row_ld8(p, 8 * (t + c * TPR), n, bf16, vec, v);
-        a[c] = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
-                          __float_as_uint(v[3]));
-        b[c] = make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]),
-                          __float_as_uint(v[7]));
+        row_ld8(p, 8 * i, n, bf16, vec, v);
+        set(c, v);
       }
     }
   }
 
   __device__ __forceinline__ void get(float v[NV][8]) const {
-    if (packed) {
 #pragma unroll
-      for (int c = 0; c < NV; ++c) unpack8(a[c], v[c]);
-    } else {
-#pragma unroll
-      for (int c = 0; c < NV; ++c) {
-        v[c][0] = __uint_as_float(a[c].x); v[c][1] = __uint_as_float(a[c].y);
-        v[c][2] = __uint_as_float(a[c].z); v[c][3] = __uint_as_float(a[c].w);
-        v[c][4] = __uint_as_float(b[c].x); v[c][5] = __uint_as_float(b[c].y);
-        v[c][6] = __uint_as_float(b[c].z); v[c][7] = __uint_as_float(b[c].w);
+    for (int c = 0; c < NV; ++c) {
+      if (MODE == 1) {
+        unpack8(a[c], v[c]);
+      } else {
+        const uint4 x = a[c], y = b[c];
+        v[c][0] = __uint_as_float(x.x); v[c][1] = __uint_as_float(x.y);
+        v[c][2] = __uint_as_float(x.z); v[c][3] = __uint_as_float(x.w);
+        v[c][4] = __uint_as_float(y.x); v[c][5] = __uint_as_float(y.y);
+        v[c][6] = __uint_as_float(y.z); v[c][7] = __uint_as_float(y.w);
       }
     }
   }
 };
+
+template <int TPR, int NV, int MODE>
+__device__ __forceinline__ void store_row(void* p, int t, int n, int bf16, int vec,
+                                          const float v[NV][8]) {
+#pragma unroll
+  for (int c = 0; c < NV; ++c) {
+    const int j = 8 * (t + c * TPR);
+    if (MODE == 0) row_st8(p, j, n, bf16, vec, v[c]);
+    else if (j < n) st8(p, j, MODE == 1, v[c]);
+  }
+}
 
 // How a matrix of rows x cols is given to teams: enough threads per row that
 // a thread holds at most 8 chunks, and whole blocks per row where there are
@@ -266,7 +278,7 @@ using C = std::integral_constant<int, I>;
 
 // f(C<TPR>, C<NV>) for the team's instance.
 template <class F>
-int with_team(Team t, F&& f) {
+int with_team_of(Team t, F&& f) {
   switch (t.tpr * 16 + t.nv) {
     case 32 * 16 + 1: return f(C<32>{}, C<1>{});
     case 32 * 16 + 2: return f(C<32>{}, C<2>{});
@@ -279,6 +291,14 @@ int with_team(Team t, F&& f) {
     case 512 * 16 + 2: return f(C<512>{}, C<2>{});
     default: return f(C<512>{}, C<4>{});
   }
+}
+
+// f(C<TPR>, C<NV>, C<MODE>): see RowRaw for the modes.
+template <class F>
+int with_team(Team t, int mode, F&& f) {
+  return with_team_of(t, [&](auto tpr, auto nv) -> int {
+    return mode == 1 ? f(tpr, nv, C<1>{}) : mode == 2 ? f(tpr, nv, C<2>{}) : f(tpr, nv, C<0>{});
+  });
 }
 
 // 8-bit rounding of a row with the largest magnitude `amax`:
