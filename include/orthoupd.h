@@ -439,12 +439,17 @@ int dion_shard_update(const ouo_mat* M, const ouo_mat* Q_state,
  * (q may differ from the exact quotient's rounding where that lies within
  * 1e-5 of a half.)  An all-zero row gets scale 0 and zeros; a row with a NaN or
  * an infinity gets scale NaN and zeros, so that every product with it is
- * NaN.  scale: host array of nmat device pointers.  X: dtype x_dtype.  Use:
+ * NaN.  scale: host array of nmat device pointers.  X: dtype x_dtype.
+ * Large transposed matrices need a workspace (16-byte aligned; 0 bytes
+ * otherwise).  Q and X must not overlap.  Use:
  * the weights after apply_update (both orders: products with W and with its
  * transpose), activations, gradients.
  */
+size_t quantize_int8_workspace_bytes(const ouo_mat* X, int x_dtype, int nmat,
+                                     int transpose);
 int quantize_int8(const ouo_mat* X, int x_dtype, const ouo_mat* Q,
-                  float* const* scale, int nmat, int transpose, void* stream);
+                  float* const* scale, int nmat, int transpose, void* ws,
+                  size_t ws_bytes, void* stream);
 
 /*
  * int8_matmul -- D[i] = diag(a_scale[i]) (A[i] B[i]^T) diag(b_scale[i]):

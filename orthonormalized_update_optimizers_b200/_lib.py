@@ -46,7 +46,7 @@ EXPORTED = (
     "dion_workspace_bytes", "dion_lowrank_step", "dion_workspace_bytes_ranks",
     "dion_lowrank_step_stats", "dion_effective_rank", "dion_shard_workspace_bytes",
     "dion_shard_red_floats", "dion_shard_project", "dion_shard_orth1", "dion_shard_orth2",
-    "dion_shard_update", "quantize_int8", "int8_matmul", "rms_norm",
+    "dion_shard_update", "quantize_int8_workspace_bytes", "quantize_int8", "int8_matmul", "rms_norm",
     "rms_norm_backward_workspace_bytes", "rms_norm_backward", "distill_loss",
     "distill_loss_backward",
 )
@@ -125,7 +125,8 @@ _PROTOS = {
     "dion_shard_orth2": (_I, [_MP, _MP, _I, _DP, _P, _P, _SZ, _P, _P, _P]),
     "dion_shard_update": (_I, [_MP, _MP, _MP, _I, _I, _DP, _P, _P, _SZ, _P, _P, _P]),
     # matrices of these are packed bytes (tokens.py)
-    "quantize_int8": (_I, [_P, _I, _P, _P, _I, _I, _P]),
+    "quantize_int8_workspace_bytes": (_SZ, [_P, _I, _I, _I]),
+    "quantize_int8": (_I, [_P, _I, _P, _P, _I, _I, _P, _SZ, _P]),
     "int8_matmul": (_I, [_P, _P, _P, _P, _P, _I, _I, _P, _P]),
     "rms_norm": (_I, [_P, _I, _P, _P, _I, _P, _I, _F, _P, _I, _P, _P, _P, _P]),
     "rms_norm_backward_workspace_bytes": (_SZ, [_I64, _I64]),

@@ -6,8 +6,6 @@
 //   dx = dh + r (w dy - h r^2 mean(w dy h)),  dw = sum over rows of dy h r
 //
 // HBM-bound: every matrix is read or written once.
-#include <mutex>
-
 #include "tokens.cuh"
 #include "umma.cuh"
 
@@ -180,13 +178,13 @@ struct NormBwdArgs {
 // same columns of all of them, so that its share of dw stays in registers
 // and leaves once, to row b of the partial sums.  MODE 1 / 2 (every matrix
 // bf16 / fp32, 16-byte accesses): DEPTH rows of dY, H and dH are on their way
-// to shared memory (cp.async, to slots that only the copying thread reads, so
-// without barriers), since the reduction of a row would otherwise leave the
+// to shared memory (cp.async, to slots that only the copying warp reads, so
+// without block barriers), since the reduction of a row would otherwise leave the
 // memory idle.
 template <int TPR, int NV, int MODE, int DEPTH>
 __global__ void __launch_bounds__(TPR) rms_bwd_kernel(const __grid_constant__ NormBwdArgs a) {
   __shared__ float red[2][TPR / 32];
-  extern __shared__ __align__(16) uint4 ring[];  // [DEPTH][3][NV][kUnits][TPR]
+  extern __shared__ __align__(16) uint4 ring[];  // [DEPTH][3][NV][TPR][kUnits]
   constexpr int kUnits = MODE == 2 ? 2 : 1;      // 16-byte pieces of a chunk
   const int t = threadIdx.x, n = (int)a.cols;
   const int dyb = MODE ? MODE == 1 : a.dy_bf16, hb = MODE ? MODE == 1 : a.h_bf16;
@@ -209,11 +207,15 @@ __global__ void __launch_bounds__(TPR) rms_bwd_kernel(const __grid_constant__ No
         if (m == 2 && !a.dH) break;
 #pragma unroll
         for (int c = 0; c < NV; ++c) {
-          if (8 * (t + c * TPR) >= n) break;
 #pragma unroll
-          for (int u = 0; u < kUnits; ++u)
-            ptx::copy16(ring + (((stage * 3 + m) * NV + c) * kUnits + u) * TPR + t,
-                        src[m] + ((t + c * TPR) * kUnits + u) * 16);
+          for (int u = 0; u < kUnits; ++u) {
+            // a warp's copies of one instruction are 512 bytes in a row, so
+            // with fp32 a lane's pieces are copied by other lanes of its warp
+            const int piece = (t & ~31) * kUnits + u * 32 + (t & 31);
+            if ((16 / kUnits) / 2 * (c * TPR * kUnits + piece) < n)
+              ptx::copy16(ring + ((stage * 3 + m) * NV + c) * kUnits * TPR + piece,
+                          src[m] + (c * TPR * kUnits + piece) * 16);
+          }
         }
         src[m] += step[m];
       }
@@ -224,9 +226,9 @@ __global__ void __launch_bounds__(TPR) rms_bwd_kernel(const __grid_constant__ No
 #pragma unroll
     for (int c = 0; c < NV; ++c) {
       const bool in = 8 * (t + c * TPR) < n;
-      const uint4* q = ring + ((stage * 3 + m) * NV + c) * kUnits * TPR + t;
+      const uint4* q = ring + (((stage * 3 + m) * NV + c) * TPR + t) * kUnits;
       r.a[c] = in ? q[0] : make_uint4(0, 0, 0, 0);
-      if (MODE != 1) r.b[MODE == 1 ? 0 : c] = in ? q[(kUnits - 1) * TPR] : make_uint4(0, 0, 0, 0);
+      if (MODE == 2) r.b[MODE == 1 ? 0 : c] = in ? q[kUnits - 1] : make_uint4(0, 0, 0, 0);
     }
   };
   int64_t ahead = blockIdx.x;
@@ -248,6 +250,7 @@ __global__ void __launch_bounds__(TPR) rms_bwd_kernel(const __grid_constant__ No
       RowRaw<TPR, NV, MODE> gr, hr;
       if (MODE) {
         asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 1) : "memory");
+        if (MODE == 2) __syncwarp();
         fetch(gr, stage, 0);
         fetch(hr, stage, 1);
         if (a.dH) fetch(dr, stage, 2);
@@ -283,6 +286,7 @@ __global__ void __launch_bounds__(TPR) rms_bwd_kernel(const __grid_constant__ No
         for (int i = 0; i < 8; ++i) g[c][i] += h[c][i];
     }
     if (MODE) {  // this stage's values are in registers
+      if (MODE == 2) __syncwarp();
       issue(ahead, stage);
       ahead += gridDim.x;
       if (++stage == DEPTH) stage = 0;
@@ -351,18 +355,8 @@ template <int TPR, int NV, int MODE, int DEPTH>
 int launch_bwd_as(const NormBwdArgs& a, unsigned grid, cudaStream_t s) {
   constexpr size_t kSmem = MODE ? (size_t)DEPTH * 3 * NV * TPR * 16 * (MODE == 2 ? 2 : 1) : 0;
   if (kSmem > 40 * 1024) {  // with the static part, past the default limit
-    static std::mutex mu;
-    static bool ready[64] = {false};
-    int dev = 0;
-    OUO_CHECK_CUDA(cudaGetDevice(&dev));
-    if (dev < 0 || dev >= 64)
-      return set_error(OUO_ERR_UNSUPPORTED, "device ordinal %d out of range", dev);
-    std::lock_guard<std::mutex> lock(mu);
-    if (!ready[dev]) {
-      OUO_CHECK_CUDA(cudaFuncSetAttribute(rms_bwd_kernel<TPR, NV, MODE, DEPTH>,
-                                          cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem));
-      ready[dev] = true;
-    }
+    static Once once;
+    OUO_TRY(once.smem(rms_bwd_kernel<TPR, NV, MODE, DEPTH>, kSmem));
   }
   rms_bwd_kernel<TPR, NV, MODE, DEPTH><<<grid, TPR, kSmem, s>>>(a);
   OUO_CHECK_LAUNCH();

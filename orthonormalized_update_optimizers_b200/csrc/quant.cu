@@ -5,7 +5,6 @@
 //
 // HBM-bound: each element is read once and leaves as one byte.
 #include <cstring>
-#include <mutex>
 
 #include "tokens.cuh"
 #include "umma.cuh"
@@ -285,20 +284,8 @@ int quant_cols(const ouo_mat& X, const ouo_mat& Q, float* scale, cudaStream_t s)
   // shared memory for two CTAs a SM; below 256 rows a CTA the cluster shrinks
   constexpr int kCached = 1600;
   constexpr size_t kSmem = (size_t)kCached * kSegBytes;
-  static std::mutex mu;
-  static bool ready[64] = {false};
-  int dev = 0;
-  OUO_CHECK_CUDA(cudaGetDevice(&dev));
-  if (dev < 0 || dev >= 64)
-    return set_error(OUO_ERR_UNSUPPORTED, "device ordinal %d out of range", dev);
-  {
-    std::lock_guard<std::mutex> lock(mu);
-    if (!ready[dev]) {
-      OUO_CHECK_CUDA(cudaFuncSetAttribute(quant_cols_kernel<BF>,
-                                          cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem));
-      ready[dev] = true;
-    }
-  }
+  static Once once;
+  OUO_TRY(once.smem(quant_cols_kernel<BF>, kSmem));
   unsigned cluster = 1;
   while (cluster < kMaxCluster && ceil_div(X.rows, (int64_t)2 * cluster) >= 128) cluster *= 2;
   QuantTArgs a;
@@ -328,11 +315,241 @@ int quant_cols(const ouo_mat& X, const ouo_mat& Q, float* scale, cudaStream_t s)
   return OUO_OK;
 }
 
+// ---- Transposed, in two launches: the columns' largest magnitudes in
+// `splits` row ranges, then the rounding, tile by tile.  X is read twice (the second
+// time from L2 as far as it fits), but both passes stream.
+
+struct QuantT2Args {
+  const void* X;
+  int64_t rows, cols, ldx;
+  int8_t* Q;
+  int64_t ldq;
+  float* scale;
+  uint32_t* part;  // [splits][cols]
+  int splits;
+  int64_t rows_split;
+  int vecx, vecq;
+  int64_t tiles_c;
+};
+
+template <int BF>
+__global__ void __launch_bounds__(256) col_amax_kernel(const __grid_constant__ QuantT2Args a) {
+  constexpr int kE = BF ? 8 : 4, kU = 16;
+  __shared__ float red[8][32][kE + 1];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t strips = (a.cols + 32 * kE - 1) / (32 * kE);
+  const int64_t split = blockIdx.x / strips, strip = blockIdx.x - split * strips;
+  const int64_t c = strip * 32 * kE + lane * kE;
+  const int64_t ra = split * a.rows_split;
+  const int64_t rb = ra + a.rows_split < a.rows ? ra + a.rows_split : a.rows;
+  float m[kE];
+#pragma unroll
+  for (int i = 0; i < kE; ++i) m[i] = 0.f;
+  if (a.vecx && c + kE <= a.cols) {
+    const char* p = reinterpret_cast<const char*>(a.X) + c * (BF ? 2 : 4);
+    const int64_t pitch = a.ldx * (BF ? 2 : 4);
+    for (int64_t r = ra + warp; r < rb; r += 8 * kU) {
+      uint4 u[kU];
+#pragma unroll
+      for (int k = 0; k < kU; ++k) {
+        u[k] = make_uint4(0, 0, 0, 0);
+        if (r + 8 * k < rb) u[k] = *reinterpret_cast<const uint4*>(p + (r + 8 * k) * pitch);
+      }
+#pragma unroll
+      for (int k = 0; k < kU; ++k) {
+        if (BF) {
+          float v[8];
+          unpack8(u[k], v);
+#pragma unroll
+          for (int i = 0; i < kE; ++i) m[i] = max_mag(m[i], v[i]);
+        } else {
+          const uint32_t w[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
+#pragma unroll
+          for (int i = 0; i < kE; ++i) m[i] = max_mag(m[i], __uint_as_float(w[i & 3]));
+        }
+      }
+    }
+  } else {
+    for (int64_t r = ra + warp; r < rb; r += 8)
+#pragma unroll
+      for (int i = 0; i < kE; ++i)
+        if (c + i < a.cols) m[i] = max_mag(m[i], ld1(a.X, r * a.ldx + c + i, BF));
+  }
+#pragma unroll
+  for (int i = 0; i < kE; ++i) red[warp][lane][i] = m[i];
+  __syncthreads();
+  for (int e = threadIdx.x; e < 32 * kE; e += 256) {
+    float v = 0.f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) v = max_mag(v, red[w][e / kE][e % kE]);
+    if (strip * 32 * kE + e < a.cols)
+      a.part[split * a.cols + strip * 32 * kE + e] = __float_as_uint(v);
+  }
+}
+
+constexpr int kMaxSplits = 32;
+
+// A tile of 128 bytes of columns x kTileRows rows goes through shared memory.
+constexpr int kTileRows = 256;
+constexpr int kOutPitch = kTileRows + 16;
+
+template <int BF>
+__global__ void __launch_bounds__(256, 4)
+quant_tile_kernel(const __grid_constant__ QuantT2Args a) {
+  constexpr int kCols = BF ? 64 : 32, kE = BF ? 8 : 4;
+  extern __shared__ __align__(16) uint32_t dyn[];
+  uint32_t(*tile)[32] = reinterpret_cast<uint32_t(*)[32]>(dyn);
+  // the tile's transpose: row e * 32 + l for column 2 l + e (fp32: l), pitch
+  // padded so that the 16-byte writes of a quarter warp lie in different banks
+  uint8_t(*out)[kOutPitch] = reinterpret_cast<uint8_t(*)[kOutPitch]>(dyn + kTileRows * 32);
+  __shared__ uint32_t cm[8][64];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t tr = blockIdx.x / a.tiles_c, tc = blockIdx.x - tr * a.tiles_c;
+  const int64_t r0 = tr * kTileRows, c0 = tc * kCols;
+  const int nr = (int)(a.rows - r0 < kTileRows ? a.rows - r0 : kTileRows);
+  const int piece = threadIdx.x & 7;
+  if (a.vecx && c0 + kCols <= a.cols) {
+    const char* p = reinterpret_cast<const char*>(a.X) + (r0 * a.ldx + c0) * (BF ? 2 : 4) + piece * 16;
+    const int64_t pitch = a.ldx * (BF ? 2 : 4);
+#pragma unroll
+    for (int k = 0; k < kTileRows / 32; ++k) {
+      const int l = (threadIdx.x >> 3) + 32 * k;
+      if (l < nr) ptx::copy16(&tile[l][piece * 4], p + l * pitch);
+    }
+  } else {
+    for (int l = threadIdx.x >> 3; l < nr; l += 32) {
+      uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+      for (int i = 0; i < kE; ++i) {
+        const int64_t c = c0 + piece * kE + i;
+        if (c >= a.cols) break;
+        const int64_t at = (r0 + l) * a.ldx + c;
+        if (BF) w[i >> 1] |= (uint32_t)reinterpret_cast<const uint16_t*>(a.X)[at] << (16 * (i & 1));
+        else w[i & 3] = reinterpret_cast<const uint32_t*>(a.X)[at];
+      }
+      *reinterpret_cast<uint4*>(&tile[l][piece * 4]) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+  // the columns' magnitudes, a group of threads per range of splits
+  {
+    constexpr int kG = 256 / kCols;
+    const int col = threadIdx.x % kCols, g = threadIdx.x / kCols;
+    uint32_t m = 0;
+    if (c0 + col < a.cols) {
+      const uint32_t* p = a.part + c0 + col;
+#pragma unroll
+      for (int k = 0; k < kMaxSplits / kG; ++k)  // all in flight together
+        if (g + k * kG < a.splits) m = max(m, p[(g + k * kG) * a.cols]);
+    }
+    cm[g][col] = m;
+  }
+  ptx::copy16_wait_all();
+  __syncthreads();
+  if (threadIdx.x < kCols) {
+    constexpr int kG = 256 / kCols;
+    uint32_t m = 0;
+#pragma unroll
+    for (int g = 0; g < kG; ++g) m = max(m, cm[g][threadIdx.x]);
+    cm[0][threadIdx.x] = m;
+    if (tr == 0 && c0 + threadIdx.x < a.cols) a.scale[c0 + threadIdx.x] = quant_of(m).scale;
+  }
+  __syncthreads();
+  const Quant q0 = quant_of(cm[0][BF ? 2 * lane : lane]);
+  const Quant q1 = BF ? quant_of(cm[0][2 * lane + 1]) : q0;
+  for (int b = warp * 16; b < nr; b += 128) {
+    uint32_t w[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) w[i] = tile[b + i][lane];
+#pragma unroll
+    for (int e = 0; e < (BF ? 2 : 1); ++e) {
+      float v[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        v[i] = __uint_as_float(!BF ? w[i] : e ? w[i] & 0xffff0000u : w[i] << 16);
+      const Quant& q = e ? q1 : q0;
+      const uint2 lo = quant8(v, q), hi = quant8(v + 8, q);
+      *reinterpret_cast<uint4*>(&out[e * 32 + lane][b]) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+    }
+  }
+  __syncthreads();
+  // whole rows of the transpose leave in order: 256 bytes each
+  for (int r = threadIdx.x >> 4; r < kCols; r += 16) {
+    const int64_t col = c0 + (BF ? 2 * (r & 31) + (r >> 5) : r);
+    if (col >= a.cols) continue;
+    int8_t* o = a.Q + col * a.ldq + r0;
+    const int l = threadIdx.x & 15;
+    if (a.vecq && 16 * l + 16 <= nr) {
+      *reinterpret_cast<uint4*>(o + 16 * l) = *reinterpret_cast<const uint4*>(&out[r][16 * l]);
+    } else if (a.vecq) {
+      for (int i = 16 * l; i < nr && i < 16 * l + 16; ++i) o[i] = (int8_t)out[r][i];
+    } else {
+      for (int i = l; i < nr; i += 16) o[i] = (int8_t)out[r][i];
+    }
+  }
+}
+
+// Row ranges of the first pass: about three blocks a SM, a function of the
+// shape alone (the workspace query needs no device).
+int amax_splits(int64_t rows, int64_t cols, int bf16) {
+  const int64_t strips = ceil_div(cols, (int64_t)(bf16 ? 256 : 128));
+  int64_t n = ceil_div((int64_t)3 * 148, strips);
+  if (n > kMaxSplits) n = kMaxSplits;
+  if (n > ceil_div(rows, (int64_t)64)) n = ceil_div(rows, (int64_t)64);
+  return (int)(n < 1 ? 1 : n);
+}
+
+// Which of the two: the clusters while the matrix is small and launches count
+// (us, clusters / two passes, bf16: 64 x 4096 3.3 / 5.0, 256 x 1024 3.4 / 5.7),
+// two passes above 3 MB, where the clusters' waits for one another do
+// (512 x 4096 8.3 / 6.4, 2048 x 4096 21.6 / 13.5, 14336 x 4096 76.4 / 61.6).
+bool two_passes(int64_t rows, int64_t cols, int bf16) {
+  return rows * cols * (bf16 ? 2 : 4) > (int64_t)3 << 20;
+}
+
+template <int BF>
+int quant_cols2(const ouo_mat& X, const ouo_mat& Q, float* scale, void* ws, cudaStream_t s) {
+  QuantT2Args a;
+  a.X = X.ptr; a.rows = X.rows; a.cols = X.cols; a.ldx = X.ld;
+  a.Q = (int8_t*)Q.ptr; a.ldq = Q.ld;
+  a.scale = scale;
+  a.part = (uint32_t*)ws;
+  a.vecx = rows16(X, BF ? 2 : 4);
+  a.vecq = rows16(Q, 1);
+  a.splits = amax_splits(X.rows, X.cols, BF);
+  a.rows_split = ceil_div(X.rows, (int64_t)a.splits);
+  a.tiles_c = ceil_div(X.cols, (int64_t)(BF ? 64 : 32));
+  const int64_t strips = ceil_div(X.cols, (int64_t)(BF ? 256 : 128));
+  const int64_t tiles = a.tiles_c * ceil_div(X.rows, (int64_t)kTileRows);
+  if (tiles > 0x7fffffff) return set_error(OUO_ERR_UNSUPPORTED, "X: too many tiles");
+  col_amax_kernel<BF><<<(unsigned)(strips * a.splits), 256, 0, s>>>(a);
+  OUO_CHECK_LAUNCH();
+  constexpr size_t kSmem = (size_t)kTileRows * 128 + (size_t)(BF ? 64 : 32) * kOutPitch;
+  static Once once;
+  OUO_TRY(once.smem(quant_tile_kernel<BF>, kSmem));
+  quant_tile_kernel<BF><<<(unsigned)tiles, 256, kSmem, s>>>(a);
+  OUO_CHECK_LAUNCH();
+  return OUO_OK;
+}
+
 }  // namespace
 }  // namespace ouo
 
+extern "C" size_t quantize_int8_workspace_bytes(const ouo_mat* X, int x_dtype, int nmat,
+                                                int transpose) {
+  using namespace ouo;
+  if (!X || !transpose || (x_dtype != OUO_F32 && x_dtype != OUO_BF16)) return 0;
+  const int bf16 = x_dtype == OUO_BF16;
+  size_t most = 0;  // the matrices of a batch follow one another
+  for (int i = 0; i < nmat; ++i)
+    if (X[i].rows > 0 && X[i].cols > 0 && two_passes(X[i].rows, X[i].cols, bf16)) {
+      const size_t b = (size_t)amax_splits(X[i].rows, X[i].cols, bf16) * (size_t)X[i].cols * 4;
+      if (b > most) most = b;
+    }
+  return most;
+}
+
 extern "C" int quantize_int8(const ouo_mat* X, int x_dtype, const ouo_mat* Q, float* const* scale,
-                             int nmat, int transpose, void* stream) {
+                             int nmat, int transpose, void* ws, size_t ws_bytes, void* stream) {
   using namespace ouo;
   clear_error();
   if (nmat < 0 || nmat > OUO_MAX_BATCH)
@@ -349,12 +566,21 @@ extern "C" int quantize_int8(const ouo_mat* X, int x_dtype, const ouo_mat* Q, fl
                            transpose ? X[i].rows : X[i].cols, "Q", i));
     OUO_TRY(validate_vec(scale[i], Q[i].rows, 4, "scale"));
   }
+  const size_t need = quantize_int8_workspace_bytes(X, x_dtype, nmat, transpose);
+  if (need > 0 && (!ws || ws_bytes < need || (uintptr_t)ws % 16 != 0))
+    return set_error(OUO_ERR_WORKSPACE, "workspace: %zu bytes needed (16-byte aligned), %zu given",
+                     need, ws ? ws_bytes : (size_t)0);
   OUO_TRY(require_sm100());
   cudaStream_t s = (cudaStream_t)stream;
   const int bf16 = x_dtype == OUO_BF16;
   if (transpose) {
     for (int i = 0; i < nmat; ++i) {
       if (X[i].cols == 0) continue;
+      if (two_passes(X[i].rows, X[i].cols, bf16)) {
+        OUO_TRY(bf16 ? quant_cols2<1>(X[i], Q[i], scale[i], ws, s)
+                     : quant_cols2<0>(X[i], Q[i], scale[i], ws, s));
+        continue;
+      }
       OUO_TRY(bf16 ? quant_cols<1>(X[i], Q[i], scale[i], s) : quant_cols<0>(X[i], Q[i], scale[i], s));
     }
     return OUO_OK;

@@ -4,6 +4,7 @@
 // rounding to 8 bits.
 #pragma once
 
+#include <mutex>
 #include <type_traits>
 
 #include "internal.h"
@@ -44,6 +45,26 @@ inline int validate_vec(const void* p, int64_t n, size_t es, const char* name) {
     return set_error(OUO_ERR_INVALID_ARG, "%s: not aligned to its element size", name);
   return OUO_OK;
 }
+
+// Raises a kernel's shared-memory limit once per device.
+struct Once {
+  std::mutex mu;
+  bool ready[64] = {false};
+  template <class K>
+  int smem(K kern, size_t bytes) {
+    int dev = 0;
+    OUO_CHECK_CUDA(cudaGetDevice(&dev));
+    if (dev < 0 || dev >= 64)
+      return set_error(OUO_ERR_UNSUPPORTED, "device ordinal %d out of range", dev);
+    std::lock_guard<std::mutex> lock(mu);
+    if (!ready[dev]) {
+      OUO_CHECK_CUDA(
+          cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes));
+      ready[dev] = true;
+    }
+    return OUO_OK;
+  }
+};
 
 inline bool rows16(const ouo_mat& m, size_t es) {
   return (uintptr_t)m.ptr % 16 == 0 && (m.rows <= 1 || (size_t)m.ld * es % 16 == 0);

@@ -20,7 +20,7 @@ from . import _lib as L
 from .binding import MatBatch
 
 __all__ = [
-    "int8_empty", "quantize_int8", "int8_matmul", "rms_norm", "rms_norm_backward",
+    "int8_empty", "quantize_int8", "quantize_int8_workspace_bytes", "int8_matmul", "rms_norm", "rms_norm_backward",
     "rms_norm_backward_workspace_bytes", "distill_loss", "distill_loss_backward",
 ]
 
@@ -104,6 +104,18 @@ def _vecs(x: Tensors, name: str, dev: int, owners) -> bytes:
     return b"".join([_ptr_bytes(_vec(t, name, dev, m.shape[0])) for t, m in zip(ts, owners)])
 
 
+def _workspace(need: int, given: Optional[torch.Tensor], dev: int, stream):
+    """(address, bytes) of a workspace: the caller's, or one allocated here
+    (the allocator keeps it for the stream that uses it)."""
+    if need == 0:
+        return None, 0
+    if given is None:
+        given = torch.empty(need, dtype=torch.uint8, device=dev)
+        if stream is not None:
+            given.record_stream(stream)
+    return _vec(given, "workspace", dev, need, torch.uint8), given.numel()
+
+
 def _run(fname: str, dev: int, stream, *args) -> None:
     """Calls the library with the tensors' device current (the first one's,
     which every other was compared with), the stream last."""
@@ -138,11 +150,20 @@ def int8_empty(rows: int, cols: int, device=None) -> torch.Tensor:
     return torch.empty((rows, pitch), dtype=torch.int8, device=dev)[:, :cols]
 
 
+def quantize_int8_workspace_bytes(X: Tensors, transpose: bool = False) -> int:
+    xs = _list(X)
+    if not xs:
+        return 0
+    return int(L.lib().quantize_int8_workspace_bytes(
+        _mats(xs, "X", xs[0].get_device()), _code(xs[0], "X"), len(xs), 1 if transpose else 0))
+
+
 def quantize_int8(X: Tensors, Q: Tensors, scale: Tensors, transpose: bool = False,
-                  stream=None) -> None:
+                  workspace: Optional[torch.Tensor] = None, stream=None) -> None:
     """Q, scale <- X in 8 bits with one scale per row, or, with ``transpose``,
     X's transpose (one scale per column of X).  X, Q and scale are tensors, or
-    lists of equal length."""
+    lists of equal length.  Large transposed matrices take a workspace
+    (allocated here unless given)."""
     xs, qs = _list(X), _list(Q)
     n = len(xs)
     if len(qs) != n:
@@ -150,9 +171,13 @@ def quantize_int8(X: Tensors, Q: Tensors, scale: Tensors, transpose: bool = Fals
     if n == 0:
         return
     dev, code = xs[0].get_device(), _code(xs[0], "X")
-    _run("quantize_int8", dev, stream, _mats(xs, "X", dev), code,
-         _mats(qs, "Q", dev, torch.int8), _vecs(scale, "scale", dev, qs), n,
-         1 if transpose else 0)
+    x = _mats(xs, "X", dev)
+    wp, wn = None, 0
+    if transpose:
+        wp, wn = _workspace(L.lib().quantize_int8_workspace_bytes(x, code, n, 1), workspace, dev,
+                            stream)
+    _run("quantize_int8", dev, stream, x, code, _mats(qs, "Q", dev, torch.int8),
+         _vecs(scale, "scale", dev, qs), n, 1 if transpose else 0, wp, wn)
 
 
 def int8_matmul(A: Tensors, a_scale: Tensors, B: Tensors, b_scale: Tensors, D: Tensors,
@@ -231,12 +256,7 @@ def rms_norm_backward(dY: torch.Tensor, H: torch.Tensor, weight: torch.Tensor,
         dh = _mat(dH, "dH", dev)
     if dweight is not None:
         dwp = _vec(dweight, "dweight", dev, cols)
-        need = rms_norm_backward_workspace_bytes(rows, cols)
-        if workspace is None:
-            workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dY.device)
-            if stream is not None:
-                workspace.record_stream(stream)
-        wp, wn = _vec(workspace, "workspace", dev, need, torch.uint8), workspace.numel()
+        wp, wn = _workspace(rms_norm_backward_workspace_bytes(rows, cols), workspace, dev, stream)
     _run("rms_norm_backward", dev, stream, dy, _code(dY, "dY"), h, _code(H, "H"), w,
          _code(weight, "weight"), rp, dh, dx, _code(dX, "dX"), dwp, wp, wn)
 

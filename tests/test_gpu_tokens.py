@@ -93,6 +93,25 @@ def test_quantize(dtype, transpose, layout):
         _check_quant(q.v.cpu().numpy().astype(np.float64), to64(s[:-1]), x64)
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("rows,cols,pad,off", [
+    (2048, 1024, 0, 0), (1100, 2049, 0, 0), (4097, 1000, 8, 0), (300, 9000, 3, 1),
+    (20001, 130, 6, 0), (60, 40000, 0, 0)])
+def test_quantize_large_transposed(rows, cols, pad, off, dtype):
+    x = torch.randn((rows, cols), generator=_rng(rows), device=DEV)
+    x[rows // 2] *= 30
+    x[:, 3] = 0
+    x[5, 4] = float("nan")
+    x = Guard(rows, cols, dtype, pad, off, x)
+    q, s = Guard(cols, rows, torch.int8, pad, off), torch.full((cols + 1,), 77.0, device=DEV)
+    ouo.quantize_int8(x.v, q.v, s, transpose=True)
+    q.check()
+    x.check()
+    assert s[-1] == 77 and torch.isnan(s[4]) and not q.v[4].any()
+    ok = np.arange(cols) != 4
+    _check_quant(to64(q.v)[ok], to64(s[:-1])[ok], to64(x.v).T[ok])
+
+
 @pytest.mark.parametrize("transpose", [False, True])
 def test_quantize_extremes(transpose):
     big, tiny = torch.finfo(F32).max, 2.0 ** -140

@@ -29,7 +29,7 @@ BAD, UNSUP, WS, NODEV = -1, -2, -3, -5
 
 def _quant(lib, x=None, q=None, s=None, dt=L.OUO_BF16, t=0, n=1):
     return lib.quantize_int8(_m(4, 8) if x is None else x, dt, _m(4, 8) if q is None else q,
-                             _v() if s is None else s, n, t, None)
+                             _v() if s is None else s, n, t, None, 0, None)
 
 
 @pytest.mark.parametrize("kw,msg", [
@@ -42,7 +42,17 @@ def _quant(lib, x=None, q=None, s=None, dt=L.OUO_BF16, t=0, n=1):
 ])
 def test_quantize_refuses(lib, kw, msg):
     assert _quant(lib, **kw) == BAD and msg in lib.ouo_last_error()
-    assert lib.quantize_int8(_m(1, 1), 0, _m(1, 1), None, 1, 0, None) == BAD
+    assert lib.quantize_int8(_m(1, 1), 0, _m(1, 1), None, 1, 0, None, 0, None) == BAD
+
+
+def test_quantize_workspace(lib):
+    big, out = _m(8192, 4096), _m(4096, 8192, 0x90000)
+    need = lib.quantize_int8_workspace_bytes(big, L.OUO_BF16, 1, 1)
+    assert need >= 4096 * 4 and lib.quantize_int8_workspace_bytes(big, L.OUO_BF16, 1, 0) == 0
+    assert lib.quantize_int8_workspace_bytes(_m(16, 64), L.OUO_BF16, 1, 1) == 0
+    for ws, n in ((None, need), (0x60000, need - 1), (0x60008, need)):
+        assert lib.quantize_int8(big, L.OUO_BF16, out, _v(), 1, 1, ws, n, None) == WS
+        assert b"workspace" in lib.ouo_last_error()
 
 
 def _mm(lib, a=None, b=None, d=None, sa=None, sb=None, dt=L.OUO_BF16, st=None):
