@@ -3,7 +3,7 @@
 //
 // Tensor cores (tcgen05.mma kind::i8, 32-bit integer accumulators in TMEM),
 // operands staged by TMA, 128 bytes of K per stage in the 128-byte swizzle:
-//   * pair kernel: clusters of two CTAs share a 256 x BN tile (each stages its
+//   * pair kernel: clusters of two CTAs share a 256 x 256 tile (each stages its
 //     128 rows of A and half of B's rows); persistent, two accumulators in
 //     TMEM, so that a tile's epilogue (scales, rounding, store) runs under the
 //     next tile's products.  Bound by the tensor pipe.
@@ -76,6 +76,68 @@ s8_simt_kernel(const int8_t* A, int64_t lda, const int8_t* B, int64_t ldb, const
 }
 
 
+// MT tokens, one or two: a warp per 2 or 4 rows of B, 16 bytes a lane and load,
+// dp4a.  Bound by reading B; the tensor-core kernels' set-up (TMEM, barriers,
+// a pipeline to fill) costs more than these few products.
+template <int MT>
+constexpr int kVecRows = MT == 1 ? 2 : 4;
+
+template <int MT>
+__global__ void __launch_bounds__(256)
+s8_vec_kernel(const int8_t* A, int64_t lda, const int8_t* B, int64_t ldb, const float* as,
+              const float* bs, void* D, int64_t ldd, int bf16, int N, int K) {
+  constexpr int kR = kVecRows<MT>;
+  const int lane = threadIdx.x & 31;
+  const int64_t n0 = ((int64_t)blockIdx.x * 8 + (threadIdx.x >> 5)) * kR;
+  if (n0 >= N) return;
+  const int8_t* b[kR];
+#pragma unroll
+  for (int r = 0; r < kR; ++r) b[r] = B + (n0 + r < N ? n0 + r : N - 1) * ldb;
+  int acc[kR][MT] = {};
+  const int k16 = K & ~15;
+  constexpr int kU = MT == 1 ? 4 : 2;
+  for (int k = 16 * lane; k < k16; k += 512 * kU) {
+    int4 x[kU][kR];
+#pragma unroll
+    for (int u = 0; u < kU; ++u)
+#pragma unroll
+      for (int r = 0; r < kR; ++r)
+        x[u][r] = k + 512 * u < k16 ? __ldcs(reinterpret_cast<const int4*>(b[r] + k + 512 * u))
+                                    : make_int4(0, 0, 0, 0);
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      if (k + 512 * u >= k16) break;
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        const int4 y = *reinterpret_cast<const int4*>(A + m * lda + k + 512 * u);
+#pragma unroll
+        for (int r = 0; r < kR; ++r) {
+          acc[r][m] = __dp4a(x[u][r].x, y.x, acc[r][m]);
+          acc[r][m] = __dp4a(x[u][r].y, y.y, acc[r][m]);
+          acc[r][m] = __dp4a(x[u][r].z, y.z, acc[r][m]);
+          acc[r][m] = __dp4a(x[u][r].w, y.w, acc[r][m]);
+        }
+      }
+    }
+  }
+  if (k16 + lane < K) {  // the last K % 16 bytes
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      const int y = A[m * lda + k16 + lane];
+#pragma unroll
+      for (int r = 0; r < kR; ++r) acc[r][m] += y * (int)b[r][k16 + lane];
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < kR; ++r)
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      const int s = __reduce_add_sync(0xffffffffu, acc[r][m]);
+      if (lane == r * MT + m && n0 + r < N)
+        st1(D, m * ldd + n0 + r, (float)s * as[m] * bs[n0 + r], bf16);
+    }
+}
+
 // ------------------------------------------------------------ tensor cores
 
 constexpr uint32_t kRowB = 128;                // bytes of K per stage
@@ -97,21 +159,18 @@ struct S8Args {
   int* status;
 };
 
-// 128-byte swizzle positions of a 32 x 32 fp32 chunk, 64-byte ones of a bf16
-// chunk: what the TMA store expects, and free of bank conflicts.
+// 128-byte swizzle position of a 4-byte column of a 32-row staging buffer: what
+// the TMA store expects, and free of bank conflicts.
 __device__ __forceinline__ int stg32(int row, int col) {
   return row * 32 + ((((col >> 2) ^ row) & 7) << 2) + (col & 3);
 }
-__device__ __forceinline__ int stg16(int row, int col) {
-  return row * 32 + ((((col >> 3) ^ (row >> 1)) & 3) << 3) + (col & 7);
-}
+constexpr int kPairN = 256;  // columns of a pair's tile
 
-template <int BN>
 struct PairCfg {
-  static constexpr uint32_t kBBytes = (BN / 2) * kRowB;  // this CTA's half of B
+  static constexpr uint32_t kBBytes = (kPairN / 2) * kRowB;  // this CTA's half of B
   static constexpr uint32_t kStage = kABytes + kBBytes;
-  static constexpr int kStages = BN == 256 ? 5 : 6;
-  static constexpr uint32_t kTmemCols = 2 * BN;
+  static constexpr int kStages = 5;
+  static constexpr uint32_t kTmemCols = 2 * kPairN;
   static constexpr uint32_t kEpi = kEpiWarps * 2 * 4096;  // two 4 KB buffers a warp
   static constexpr size_t kSmem = 1024 + (size_t)kStages * kStage + kEpi + 512;
 };
@@ -126,11 +185,10 @@ __device__ __forceinline__ void decode(const S8Args& a, int64_t t, int* ti, int*
   *ti = first + (int)(r - (int64_t)*tj * rows);
 }
 
-template <int BN>
 __global__ void __launch_bounds__(kPairThreads, 1)
 s8_pair_kernel(const __grid_constant__ S8Args a) {
-  using C = PairCfg<BN>;
-  constexpr uint32_t kIdesc = ptx::instr_desc_s8(BN, 256);
+  using C = PairCfg;
+  constexpr uint32_t kIdesc = ptx::instr_desc_s8(kPairN, 256);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
@@ -181,7 +239,7 @@ s8_pair_kernel(const __grid_constant__ S8Args a) {
       int ti, tj;
       decode(a, t, &ti, &tj);
       const int32_t arow = ti * 256 + (int32_t)rank * 128;
-      const int32_t brow = tj * BN + (int32_t)rank * (BN / 2);
+      const int32_t brow = tj * kPairN + (int32_t)rank * (kPairN / 2);
       for (int kb = 0; kb < a.nk; ++kb) {
         if (!ptx::mbar_wait(&empty[stage], phase ^ 1, abort_flag)) {
           ok = false;
@@ -226,7 +284,7 @@ s8_pair_kernel(const __grid_constant__ S8Args a) {
         break;
       }
       ptx::tc_fence_after();
-      const uint32_t d = tmem + buf * BN;
+      const uint32_t d = tmem + buf * kPairN;
       for (int kb = 0; kb < a.nk; ++kb) {
         if (!ptx::mbar_wait(&full[stage], phase, abort_flag)) {
           ok = false;
@@ -254,7 +312,7 @@ s8_pair_kernel(const __grid_constant__ S8Args a) {
   } else if (warp >= 2) {
     // epilogue: one TMEM lane quarter and half of the columns per warp
     const uint32_t q = (uint32_t)(warp & 3), half = (uint32_t)((warp - 2) >> 2);
-    constexpr int kCh = BN / 64;  // 32-column chunks per warp
+    constexpr int kCh = kPairN / 64;  // 32-column chunks per warp
     const uint32_t tempty_lead = ptx::mapa(ptx::smem_u32(tempty), 0);
     float* const stg0 = reinterpret_cast<float*>(epi + (warp - 2) * 8192);
     uint32_t nst = 0;
@@ -264,7 +322,7 @@ s8_pair_kernel(const __grid_constant__ S8Args a) {
       decode(a, t, &ti, &tj);
       const uint32_t buf = (uint32_t)(local & 1);
       const int row0 = ti * 256 + (int)rank * 128 + (int)q * 32;
-      const int col0 = tj * BN + (int)half * (BN / 2);
+      const int col0 = tj * kPairN + (int)half * (kPairN / 2);
       const float as = row0 + lane < a.M ? a.as[row0 + lane] : 0.f;
       float bs[kCh];  // lane's column of each chunk
 #pragma unroll
@@ -286,35 +344,39 @@ s8_pair_kernel(const __grid_constant__ S8Args a) {
         const int gj0 = col0 + c * 32;
         if (row0 >= a.M || gj0 >= a.N) continue;
         float v[32];
-        ptx::tmem_ld32(tmem + ((q * 32u) << 16) + buf * BN + half * (BN / 2) + c * 32, v);
+        ptx::tmem_ld32(tmem + ((q * 32u) << 16) + buf * kPairN + half * (kPairN / 2) + c * 32, v);
 #pragma unroll
         for (int j = 0; j < 32; ++j)
           v[j] = (float)__float_as_int(v[j]) * as * __shfl_sync(0xffffffffu, bs[c], j);
         float* stg = stg0 + (nst & 1u) * 1024;
         if (a.tma_out) {
-          // the store before last has finished reading this buffer
-          if (lane == 0) ptx::bulk_wait_read1();
-          __syncwarp();
+          // a staging buffer is 32 rows of 128 bytes: 32 fp32 columns, or 64
+          // bf16 ones, the second chunk filling the rows' second half
+          const bool lo = !a.bf16 || (c & 1) == 0;
+          const bool last = !a.bf16 || (c & 1) == 1 || gj0 + 32 >= a.N;
+          if (lo) {  // the store before last has finished reading the buffer
+            if (lane == 0) ptx::bulk_wait_read1();
+            __syncwarp();
+          }
           if (!a.bf16) {
 #pragma unroll
             for (int j = 0; j < 32; j += 4)
               *reinterpret_cast<float4*>(stg + stg32(lane, j)) =
                   make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
           } else {
-            uint16_t* h = reinterpret_cast<uint16_t*>(stg);
 #pragma unroll
             for (int j = 0; j < 32; j += 8)
-              *reinterpret_cast<uint4*>(h + stg16(lane, j)) =
-                  make_uint4(pack_bf16x2(v[j], v[j + 1]), pack_bf16x2(v[j + 2], v[j + 3]),
-                             pack_bf16x2(v[j + 4], v[j + 5]), pack_bf16x2(v[j + 6], v[j + 7]));
+              *reinterpret_cast<uint4*>(stg + stg32(lane, (c & 1) * 16 + j / 2)) = pack8(v + j);
           }
-          ptx::fence_async_shared();
-          __syncwarp();
-          if (lane == 0) {
-            ptx::tma_store_2d(&a.tmD, stg, gj0, row0);
-            ptx::bulk_commit();
+          if (last) {
+            ptx::fence_async_shared();
+            __syncwarp();
+            if (lane == 0) {
+              ptx::tma_store_2d(&a.tmD, stg, lo ? gj0 : gj0 - 32, row0);
+              ptx::bulk_commit();
+            }
+            ++nst;
           }
-          ++nst;
         } else {
           __syncwarp();
 #pragma unroll
@@ -345,6 +407,8 @@ s8_pair_kernel(const __grid_constant__ S8Args a) {
 // ------------------------------------------------------------ split kernel
 
 constexpr int kSplitThreads = 192;
+using C0 = std::integral_constant<int, 0>;
+using C1 = std::integral_constant<int, 1>;
 
 struct SplitArgs {
   CUtensorMap tmR, tmT;  // R: 128 rows a tile; T: BN rows a tile
@@ -356,7 +420,7 @@ struct SplitArgs {
   int t_rows;   // D's rows are T's rows (else R's)
   int R, T, nk, nk_cta;
   int tiles_t;
-  int vec;      // D rows allow 4-element stores
+  int vec;      // D rows on 16-byte boundaries
   int* status;
 };
 
@@ -364,13 +428,14 @@ template <int BN>
 struct SplitCfg {
   static constexpr uint32_t kTBytes = BN * kRowB;
   static constexpr uint32_t kStage = kABytes + kTBytes;
-  static constexpr int kStages = 4;
+  // two CTAs a SM
+  static constexpr int kStages = BN == 16 ? 6 : BN == 32 ? 5 : BN == 64 ? 4 : 3;
   static constexpr uint32_t kTmemCols = BN < 32 ? 32 : BN;
   static constexpr size_t kSmem = 1024 + (size_t)kStages * kStage + 256;
   static_assert((size_t)BN * 512 <= (size_t)kStages * kStage, "partial sums reuse the stages");
 };
 
-template <int BN>
+template <int BN, int NS /* CTAs of the cluster, which divide K */>
 __global__ void __launch_bounds__(kSplitThreads)
 s8_split_kernel(const __grid_constant__ SplitArgs a) {
   using C = SplitCfg<BN>;
@@ -383,12 +448,12 @@ s8_split_kernel(const __grid_constant__ SplitArgs a) {
   uint64_t* done = empty + C::kStages;
   uint32_t* holder = reinterpret_cast<uint32_t*>(done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(holder + 1);
-  int* part = reinterpret_cast<int*>(smem);  // [BN][128], after the products
+  __shared__ __align__(16) float rs[128];
+  __shared__ float ts[BN / NS];
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  uint32_t rank = ptx::cluster_ctarank(), nsplit;
-  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(nsplit));
-  const int tile = (int)(blockIdx.x / nsplit);
+  const uint32_t rank = NS > 1 ? ptx::cluster_ctarank() : 0u;
+  const int tile = (int)(blockIdx.x / NS);
   const int r0 = tile / a.tiles_t * 128, t0 = tile % a.tiles_t * BN;
   const int kb0 = (int)rank * a.nk_cta, kb1 = min(a.nk, kb0 + a.nk_cta);
 
@@ -411,6 +476,14 @@ s8_split_kernel(const __grid_constant__ SplitArgs a) {
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = *holder;
+
+  constexpr int kPer = BN / NS;            // T rows that this CTA writes
+  const int first = t0 + (int)rank * kPer;  // its first one
+  // the scales arrive under the products
+  for (int i = threadIdx.x; i < kPer; i += kSplitThreads)
+    ts[i] = first + i < a.T ? a.ts[first + i] : 0.f;
+  if (threadIdx.x < 128) rs[threadIdx.x] = r0 + threadIdx.x < a.R ? a.rs[r0 + threadIdx.x] : 0.f;
+  __syncwarp();
 
   if (warp == 0 && lane == 0) {
     uint32_t stage = 0, phase = 0;
@@ -460,79 +533,110 @@ s8_split_kernel(const __grid_constant__ SplitArgs a) {
     ptx::mbar_wait_timed(done, 0, kWaitLimitNs);
   }
   __syncwarp();
-  __syncthreads();  // the products are done, the stages are free
-  const uint32_t q = (uint32_t)(warp & 3);
+  // The products are done and the stages free, in every CTA of the cluster.
+  if (NS > 1) ptx::cluster_sync();
+  else __syncthreads();
+  const uint32_t q = (uint32_t)(warp & 3);  // TMEM lanes 32 q .. + 31
+  constexpr int kStep = BN < 32 ? 16 : 32;
+  if (warp >= 2) ptx::tc_fence_after();
+  auto sums = [&](int c, float v[kStep]) {  // columns c .. of the lane's row
+    if (kb1 > kb0) {
+      if (kStep == 16) ptx::tmem_ld16(tmem + ((q * 32u) << 16) + c, v);
+      else ptx::tmem_ld32(tmem + ((q * 32u) << 16) + c, v);
+    } else {
+#pragma unroll
+      for (int j = 0; j < kStep; ++j) v[j] = 0.f;
+    }
+  };
+  // Each CTA owns kPer of the T rows: it gets every CTA's sums for them (remote
+  // stores, which nobody waits for), adds and writes them.
+  int* part = reinterpret_cast<int*>(smem);  // [NS][kPer][128]
   if (warp >= 2) {
-    ptx::tc_fence_after();
-    constexpr int kStep = BN < 32 ? 16 : 32;
-#pragma unroll 1
+    uint32_t to[NS];
+#pragma unroll
+    for (int o = 0; o < NS; ++o) {
+      const uint32_t at = ptx::smem_u32(part + (int)rank * kPer * 128 + q * 32 + lane);
+      to[o] = NS > 1 ? ptx::mapa(at, o) : at;
+    }
+#pragma unroll
     for (int c = 0; c < BN; c += kStep) {
       float v[kStep];
-      if (kb1 > kb0) {
-        if (kStep == 16) ptx::tmem_ld16(tmem + ((q * 32u) << 16) + c, v);
-        else ptx::tmem_ld32(tmem + ((q * 32u) << 16) + c, v);
-      } else {
+      sums(c, v);
 #pragma unroll
-        for (int j = 0; j < kStep; ++j) v[j] = 0.f;
+      for (int j = 0; j < kStep; ++j) {
+        const uint32_t at = to[(c + j) / kPer] + (uint32_t)((c + j) % kPer) * 512u;
+        if (NS > 1) ptx::st_cluster_int(at, __float_as_int(v[j]));
+        else part[(c + j) * 128 + q * 32 + lane] = __float_as_int(v[j]);
       }
-#pragma unroll
-      for (int j = 0; j < kStep; ++j)
-        part[(c + j) * 128 + q * 32 + lane] = __float_as_int(v[j]);
     }
-    ptx::tc_fence_before();
   }
   __syncwarp();
-  ptx::cluster_sync();
-  // The CTAs of a cluster divide the T rows of the tile: CTA `rank` sums and
-  // writes rows rank, rank + nsplit, ...
-  if (warp >= 2) {
-    const uint32_t base = ptx::smem_u32(part);
-    if (a.t_rows) {
-      const int r = r0 + 4 * lane;
-      float rs[4];
+  if (NS > 1) ptx::cluster_sync();
+  else __syncthreads();
+  // Branched on the output's type once: a branch per element costs more than
+  // the element (a 128 x 128 tile took 12,000 cycles to write).
+  {
+    const int n = min(kPer, a.T - first);
+    auto write = [&](auto bf) {
+      constexpr int BF = decltype(bf)::value;
+      using E = std::conditional_t<BF, __nv_bfloat16, float>;
+      if (a.t_rows) {
+        const int r = r0 + 4 * lane;
+        const bool wide = a.vec && r + 3 < a.R;
+        const float4 s4 = *reinterpret_cast<const float4*>(rs + 4 * lane);
+        E* d = reinterpret_cast<E*>(a.D) + (int64_t)first * a.ldd + r;
+#pragma unroll 4
+        for (int j = warp; j < n; j += kSplitThreads / 32) {
+          int4 x = make_int4(0, 0, 0, 0);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) rs[i] = r + i < a.R ? a.rs[r + i] : 0.f;
-      for (int j = (int)rank + (int)nsplit * (warp - 2); j < BN && t0 + j < a.T;
-           j += 4 * (int)nsplit) {
-        int4 s = make_int4(0, 0, 0, 0);
-        for (uint32_t p = 0; p < nsplit; ++p) {
-          const int4 x = ptx::ld_cluster_int4(
-              ptx::mapa(base + (uint32_t)(j * 128 + 4 * lane) * 4u, p));
-          s.x += x.x; s.y += x.y; s.z += x.z; s.w += x.w;
+          for (int p = 0; p < NS; ++p) {
+            const int4 y = *reinterpret_cast<const int4*>(part + (p * kPer + j) * 128 + 4 * lane);
+            x.x += y.x; x.y += y.y; x.z += y.z; x.w += y.w;
+          }
+          const float t = ts[j];
+          const float v[4] = {(float)x.x * t * s4.x, (float)x.y * t * s4.y, (float)x.z * t * s4.z,
+                              (float)x.w * t * s4.w};
+          E* o = d + (int64_t)j * a.ldd;
+          if (wide) {
+            if (BF) *reinterpret_cast<uint2*>(o) = make_uint2(pack2(v[0], v[1]), pack2(v[2], v[3]));
+            else *reinterpret_cast<float4*>(o) = make_float4(v[0], v[1], v[2], v[3]);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (r + k < a.R) o[k] = (E)v[k];
+          }
         }
-        const float ts = a.ts[t0 + j];
-        // (sum * a_scale) * b_scale: T is A here
-        const float v[4] = {(float)s.x * ts * rs[0], (float)s.y * ts * rs[1],
-                            (float)s.z * ts * rs[2], (float)s.w * ts * rs[3]};
-        const int64_t o = (int64_t)(t0 + j) * a.ldd + r;
-        if (a.vec && r + 3 < a.R) {
-          if (a.bf16)
-            *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.D) + o) =
-                make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
-          else
-            *reinterpret_cast<float4*>(reinterpret_cast<float*>(a.D) + o) =
-                make_float4(v[0], v[1], v[2], v[3]);
+      } else if (threadIdx.x < 128 && r0 + threadIdx.x < a.R) {
+        const int row = threadIdx.x;
+        const float s = rs[row];
+        E* d = reinterpret_cast<E*>(a.D) + (int64_t)(r0 + row) * a.ldd + first;
+        auto value = [&](int j) {
+          int x = 0;
+#pragma unroll
+          for (int p = 0; p < NS; ++p) x += part[(p * kPer + j) * 128 + row];
+          return (float)x * s * ts[j];
+        };
+        if (kPer % 8 == 0 && a.vec && n == kPer) {
+#pragma unroll 2
+          for (int j = 0; j < kPer; j += 8) {
+            float v[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] = value(j + k);
+            st8(d, j, BF, v);
+          }
         } else {
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (r + i < a.R) st1(a.D, o + i, v[i], a.bf16);
+          for (int j = 0; j < kPer; ++j)
+            if (j < n) d[j] = (E)value(j);
         }
       }
-    } else {
-      const int row = (warp - 2) * 32 + lane;
-      const float rs = r0 + row < a.R ? a.rs[r0 + row] : 0.f;
-      const int per = (BN + (int)nsplit - 1) / (int)nsplit;
-      for (int j = (int)rank * per; j < BN && j < ((int)rank + 1) * per && t0 + j < a.T; ++j) {
-        int s = 0;
-        for (uint32_t p = 0; p < nsplit; ++p)
-          s += ptx::ld_cluster_int(ptx::mapa(base + (uint32_t)(j * 128 + row) * 4u, p));
-        if (r0 + row < a.R)
-          st1(a.D, (int64_t)(r0 + row) * a.ldd + t0 + j, (float)s * rs * a.ts[t0 + j], a.bf16);
-      }
-    }
+    };
+    if (a.bf16) write(C1{});
+    else write(C0{});
   }
+  if (warp >= 2) ptx::tc_fence_before();
   __syncwarp();
-  ptx::cluster_sync();  // peers have read this CTA's sums
+  __syncthreads();
   if (warp == 1) {
     ptx::tc_fence_after();
     ptx::tmem_dealloc(tmem, C::kTmemCols);
@@ -634,45 +738,43 @@ struct Product {
   int* status;
 };
 
-template <int BN>
 int run_pair(const Product& p, cudaStream_t s) {
-  using C = PairCfg<BN>;
+  using C = PairCfg;
   static Setup st;
   int slots = 0;
-  OUO_TRY(setup(st, s8_pair_kernel<BN>, kPairThreads, C::kSmem, 2, &slots));
+  OUO_TRY(setup(st, s8_pair_kernel, kPairThreads, C::kSmem, 2, &slots));
   S8Args a;
   memset(&a, 0, sizeof(a));
   OUO_TRY(map_s8(&a.tmA, p.A, 128));
-  OUO_TRY(map_s8(&a.tmB, p.B, BN / 2));
+  OUO_TRY(map_s8(&a.tmB, p.B, kPairN / 2));
   const size_t es = p.bf16 ? 2 : 4;
   a.tma_out = rows16(p.D, es) ? 1 : 0;
   if (a.tma_out)
     OUO_TRY(make_map(&a.tmD, p.D,
                      p.bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
-                     es, 32, 32, p.bf16 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B));
+                     es, p.bf16 ? 64 : 32, 32, CU_TENSOR_MAP_SWIZZLE_128B));
   a.as = p.as; a.bs = p.bs;
   a.D = p.D.ptr; a.ldd = p.D.ld; a.bf16 = p.bf16;
   a.M = (int)p.D.rows; a.N = (int)p.D.cols;
   a.nk = (int)ceil_div(p.A.cols, (int64_t)kRowB);
   a.tiles_m = (int)ceil_div(p.D.rows, 256);
-  a.tiles_n = (int)ceil_div(p.D.cols, BN);
+  a.tiles_n = (int)ceil_div(p.D.cols, kPairN);
   a.total = (int64_t)a.tiles_m * a.tiles_n;
   a.status = p.status;
   const int64_t n = a.total < slots ? a.total : slots;
   cudaLaunchAttribute attr[1];
   cudaLaunchConfig_t cfg = config((unsigned)(2 * n), kPairThreads, C::kSmem, s, 2, attr);
-  OUO_CHECK_CUDA(cudaLaunchKernelEx(&cfg, s8_pair_kernel<BN>, a));
+  OUO_CHECK_CUDA(cudaLaunchKernelEx(&cfg, s8_pair_kernel, a));
   OUO_CHECK_LAUNCH();
   return OUO_OK;
 }
 
 // t_rows: T is A (D's rows), R is B; else the other way round.
-template <int BN>
-int run_split(const Product& p, bool t_rows, unsigned nsplit, cudaStream_t s) {
+template <int BN, int NS>
+int run_split(const Product& p, bool t_rows, cudaStream_t s) {
   using C = SplitCfg<BN>;
-  static Setup st;
-  int slots = 0;
-  OUO_TRY(setup(st, s8_split_kernel<BN>, kSplitThreads, C::kSmem, 1, &slots));
+  static Once once;
+  OUO_TRY(once.smem((s8_split_kernel<BN, NS>), C::kSmem));
   SplitArgs a;
   memset(&a, 0, sizeof(a));
   const ouo_mat& R = t_rows ? p.B : p.A;
@@ -685,18 +787,27 @@ int run_split(const Product& p, bool t_rows, unsigned nsplit, cudaStream_t s) {
   a.t_rows = t_rows ? 1 : 0;
   a.R = (int)R.rows; a.T = (int)T.rows;
   a.nk = (int)ceil_div(R.cols, (int64_t)kRowB);
-  a.nk_cta = (int)ceil_div(a.nk, (int64_t)nsplit);
+  a.nk_cta = (int)ceil_div(a.nk, (int64_t)NS);
   a.tiles_t = (int)ceil_div(T.rows, BN);
-  const size_t es4 = p.bf16 ? 8 : 16;
-  a.vec = (uintptr_t)p.D.ptr % es4 == 0 && (p.D.rows <= 1 || p.D.ld % 4 == 0);
+  a.vec = rows16(p.D, p.bf16 ? 2 : 4);
   a.status = p.status;
   const int64_t tiles = ceil_div(R.rows, 128) * (int64_t)a.tiles_t;
-  if (tiles * nsplit > 0x7fffffff) return set_error(OUO_ERR_UNSUPPORTED, "D: too many tiles");
+  if (tiles * NS > 0x7fffffff) return set_error(OUO_ERR_UNSUPPORTED, "D: too many tiles");
   cudaLaunchAttribute attr[1];
-  cudaLaunchConfig_t cfg = config((unsigned)(tiles * nsplit), kSplitThreads, C::kSmem, s, nsplit, attr);
-  OUO_CHECK_CUDA(cudaLaunchKernelEx(&cfg, s8_split_kernel<BN>, a));
+  cudaLaunchConfig_t cfg = config((unsigned)(tiles * NS), kSplitThreads, C::kSmem, s, NS, attr);
+  OUO_CHECK_CUDA(cudaLaunchKernelEx(&cfg, s8_split_kernel<BN, NS>, a));
   OUO_CHECK_LAUNCH();
   return OUO_OK;
+}
+
+template <int BN>
+int run_split(const Product& p, bool t_rows, int nsplit, cudaStream_t s) {
+  switch (nsplit) {
+    case 1: return run_split<BN, 1>(p, t_rows, s);
+    case 2: return run_split<BN, 2>(p, t_rows, s);
+    case 4: return run_split<BN, 4>(p, t_rows, s);
+    default: return run_split<BN, 8>(p, t_rows, s);
+  }
 }
 
 int run_simt(const Product& p, cudaStream_t s) {
@@ -709,20 +820,43 @@ int run_simt(const Product& p, cudaStream_t s) {
   return OUO_OK;
 }
 
+template <int MT>
+int run_vec(const Product& p, cudaStream_t s) {
+  const int64_t blocks = ceil_div(p.D.cols, (int64_t)8 * kVecRows<MT>);
+  if (blocks > 0x7fffffff) return set_error(OUO_ERR_UNSUPPORTED, "D: too many columns");
+  s8_vec_kernel<MT><<<(unsigned)blocks, 256, 0, s>>>(
+      (const int8_t*)p.A.ptr, p.A.ld, (const int8_t*)p.B.ptr, p.B.ld, p.as, p.bs, p.D.ptr, p.D.ld,
+      p.bf16, (int)p.D.cols, (int)p.A.cols);
+  OUO_CHECK_LAUNCH();
+  return OUO_OK;
+}
+
 int product(const Product& p, cudaStream_t s) {
   const int64_t M = p.D.rows, N = p.D.cols, K = p.A.cols;
   if (M == 0 || N == 0) return OUO_OK;
   if (K == 0 || !rows16(p.A, 1) || !rows16(p.B, 1)) return run_simt(p, s);
-  const int64_t pairs = num_sms() / 2;
-  const int64_t tiles = ceil_div(M, 256) * ceil_div(N, 256);
-  if (M > 128 && N > 128 && tiles >= pairs) return run_pair<256>(p, s);
-  // T is the side with fewer rows, A unless B's rows are few
+  // One or two tokens: 11.4 / 13.4 us at 14336 x 4096 against 14.9 in the split
+  // kernel; four are its (21.0 against 15.0).
+  if (M == 1) return run_vec<1>(p, s);
+  if (M == 2) return run_vec<2>(p, s);
+  // Pair tiles once they occupy two thirds of the SMs: 17.6 us at 1024 x 4096 x
+  // 4096 (64 tiles) against 20.5 in the split kernel, 17.1 against 15.8 at half
+  // the rows (32 tiles).
+  const int64_t sms = num_sms();
+  if (M > 128 && N > 128 && 3 * ceil_div(M, 256) * ceil_div(N, 256) >= sms) return run_pair(p, s);
+  // T is the side with fewer rows, A unless B's rows are few.
   const bool t_rows = M <= N || N > 128;
   const int64_t T = t_rows ? M : N, R = t_rows ? N : M;
   const int bn = T <= 16 ? 16 : T <= 32 ? 32 : T <= 64 ? 64 : 128;
+  // K is divided while the CTAs fit one to an SM and keep enough of it: the
+  // join grows with the tile (128 x 4096 x 4096, 32 tiles: 18.3 / 13.3 / 11.6 /
+  // 15.9 us in 1 / 2 / 4 / 8; 1 x 1024 x 4096, 8 tiles: 12.3 / 7.9 / 5.8 / 4.9).  In
+  // two as long as both halves fit two to an SM (512 x 4096 x 4096: 18.3 / 15.8).
   const int64_t st = ceil_div(R, 128) * ceil_div(T, bn), nk = ceil_div(K, (int64_t)kRowB);
-  unsigned split = 1;
-  while (split < 8 && st * split < 2 * num_sms() && nk / (2 * split) >= 2) split *= 2;
+  const int64_t least = bn <= 32 ? 2 : 8;
+  int split = 1;
+  while (split < 8 && st * 2 * split <= sms && nk / (2 * split) >= (split == 1 ? 2 : least)) split *= 2;
+  if (split == 1 && st <= sms && nk >= 4) split = 2;
   switch (bn) {
     case 16: return run_split<16>(p, t_rows, split, s);
     case 32: return run_split<32>(p, t_rows, split, s);
