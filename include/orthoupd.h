@@ -423,8 +423,10 @@ int dion_shard_update(const ouo_mat* M, const ouo_mat* Q_state,
  *
  * Token matrices: rows are tokens.  Unlike the batches above they may be
  * empty (0 rows, or 0 columns where a call says so); pointers of empty
- * matrices are not looked at.  Any row pitch and any alignment to the
- * element size is taken; rows that start on 16-byte boundaries are faster.
+ * matrices are not looked at.  At most 2^30 rows and columns.  Any row pitch
+ * and any alignment to the element size is taken; rows that start on 16-byte
+ * boundaries are faster (much, for int8_matmul, whose tensor-core kernels
+ * need them in A and B).
  * Sums, norms and softmax statistics are held in fp32 or wider.
  * 8-bit matrices hold signed integers, one byte each (`ld` in bytes).
  */
@@ -478,7 +480,8 @@ int int8_matmul(const ouo_mat* A, const float* const* a_scale,
  * in 8 bits as quantize_int8 without transposition); rstd (optional, r per
  * row, for the gradient).  residual and H share h_dtype; H may be the residual
  * or X itself (same pointer, type and pitch).  Other outputs must not overlap
- * inputs.  weight: device vector of cols elements, w_dtype.
+ * inputs.  weight: device vector of cols elements, w_dtype.  The squares are
+ * summed in fp32: |h| is expected below 1e16 or so.
  *
  * rms_norm_backward -- dY: gradient of y (through the 8-bit rounding it
  * passes unchanged), H and rstd as above, dH: gradient that reaches h past

@@ -437,8 +437,7 @@ int distill_loss_backward(const ouo_mat* S, int s_dtype, const ouo_mat* teacher,
   OUO_TRY(validate_dtype(ds_dtype, "dS"));
   OUO_TRY(validate_tokens(*dS, elem_size(ds_dtype), "dS", 0));
   OUO_TRY(validate_shape(*dS, S->rows, S->cols, "dS", 0));
-  if (dS->ptr == S->ptr && (ds_dtype != s_dtype || dS->ld != S->ld) && S->rows > 0)
-    return set_error(OUO_ERR_INVALID_ARG, "dS in place of S needs S's type and row pitch");
+  OUO_TRY(validate_in_place(*dS, ds_dtype, *S, s_dtype, "dS and S"));
   OUO_TRY(validate_vec(lse, S->rows, 4, "lse"));
   OUO_TRY(validate_vec(dloss, S->rows, 4, "dloss"));
   if (S->rows == 0) return OUO_OK;

@@ -152,7 +152,7 @@ struct S8Args {
   const float* bs;
   void* D;
   int64_t ldd;
-  int bf16, tma_out;
+  int bf16, tma_out, ragged;
   int M, N, nk;          // nk: K in stages
   int tiles_m, tiles_n;
   int64_t total;
@@ -349,7 +349,10 @@ s8_pair_kernel(const __grid_constant__ S8Args a) {
         for (int j = 0; j < 32; ++j)
           v[j] = (float)__float_as_int(v[j]) * as * __shfl_sync(0xffffffffu, bs[c], j);
         float* stg = stg0 + (nst & 1u) * 1024;
-        if (a.tma_out) {
+        // The TMA store clips a box at 16 bytes, not at the element: a box over
+        // D's last column goes by TMA only if the row ends on that boundary.
+        const int box = a.bf16 ? gj0 - (c & 1) * 32 : gj0;
+        if (a.tma_out && (!a.ragged || box + (a.bf16 ? 64 : 32) <= a.N)) {
           // a staging buffer is 32 rows of 128 bytes: 32 fp32 columns, or 64
           // bf16 ones, the second chunk filling the rows' second half
           const bool lo = !a.bf16 || (c & 1) == 0;
@@ -378,15 +381,27 @@ s8_pair_kernel(const __grid_constant__ S8Args a) {
             ++nst;
           }
         } else {
+          if (lane == 0) ptx::bulk_wait_read0();  // stores by TMA have read the buffers
           __syncwarp();
 #pragma unroll
           for (int j = 0; j < 32; j += 4)
             *reinterpret_cast<float4*>(stg + stg32(lane, j)) =
                 make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
           __syncwarp();
-          if (gj0 + lane < a.N)
-            for (int r = 0; r < 32 && row0 + r < a.M; ++r)
-              st1(a.D, (int64_t)(row0 + r) * a.ldd + gj0 + lane, stg[stg32(r, lane)], a.bf16);
+          if (gj0 + lane < a.N) {
+            const int rows = min(32, a.M - row0);
+            const int64_t o = (int64_t)row0 * a.ldd + gj0 + lane;
+            if (a.bf16) {
+              __nv_bfloat16* d = reinterpret_cast<__nv_bfloat16*>(a.D) + o;
+#pragma unroll 8
+              for (int r = 0; r < rows; ++r) d[r * a.ldd] = __float2bfloat16_rn(stg[stg32(r, lane)]);
+            } else {
+              float* d = reinterpret_cast<float*>(a.D) + o;
+#pragma unroll 8
+              for (int r = 0; r < rows; ++r) d[r * a.ldd] = stg[stg32(r, lane)];
+            }
+          }
+          __syncwarp();
         }
       }
       ptx::tc_fence_before();
@@ -749,6 +764,7 @@ int run_pair(const Product& p, cudaStream_t s) {
   OUO_TRY(map_s8(&a.tmB, p.B, kPairN / 2));
   const size_t es = p.bf16 ? 2 : 4;
   a.tma_out = rows16(p.D, es) ? 1 : 0;
+  a.ragged = p.D.cols * es % 16 != 0;
   if (a.tma_out)
     OUO_TRY(make_map(&a.tmD, p.D,
                      p.bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,

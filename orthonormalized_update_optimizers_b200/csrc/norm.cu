@@ -403,10 +403,12 @@ int rms_norm(const ouo_mat* X, int x_dtype, const ouo_mat* residual, const ouo_m
     OUO_TRY(validate_dtype(h_dtype, "H"));
     OUO_TRY(validate_tokens(*H, elem_size(h_dtype), "H", 0));
     OUO_TRY(validate_shape(*H, T, n, "H", 0));
+    OUO_TRY(validate_in_place(*H, h_dtype, *X, x_dtype, "H and X"));
   }
   if (residual) {
     OUO_TRY(validate_tokens(*residual, elem_size(h_dtype), "residual", 0));
     OUO_TRY(validate_shape(*residual, T, n, "residual", 0));
+    OUO_TRY(validate_in_place(*H, h_dtype, *residual, h_dtype, "H and residual"));
   }
   if (Y) {
     OUO_TRY(validate_dtype(y_dtype, "Y"));
@@ -483,6 +485,8 @@ int rms_norm_backward(const ouo_mat* dY, int dy_dtype, const ouo_mat* H, int h_d
   OUO_TRY(validate_shape(*H, T, n, "H", 0));
   OUO_TRY(validate_tokens(*dX, elem_size(dx_dtype), "dX", 0));
   OUO_TRY(validate_shape(*dX, T, n, "dX", 0));
+  OUO_TRY(validate_in_place(*dX, dx_dtype, *dY, dy_dtype, "dX and dY"));
+  if (dH) OUO_TRY(validate_in_place(*dX, dx_dtype, *dH, dx_dtype, "dX and dH"));
   if (dH) {
     OUO_TRY(validate_tokens(*dH, elem_size(dx_dtype), "dH", 0));
     OUO_TRY(validate_shape(*dH, T, n, "dH", 0));

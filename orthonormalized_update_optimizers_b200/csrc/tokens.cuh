@@ -18,7 +18,7 @@ inline int validate_tokens(const ouo_mat& m, size_t es, const char* name, int i)
   if (m.rows < 0 || m.cols < 0)
     return set_error(OUO_ERR_INVALID_ARG, "%s[%d]: negative shape %lld x %lld", name, i,
                      (long long)m.rows, (long long)m.cols);
-  if (m.rows >= (int64_t)1 << 31 || m.cols >= (int64_t)1 << 31)
+  if (m.rows > (int64_t)1 << 30 || m.cols > (int64_t)1 << 30)
     return set_error(OUO_ERR_INVALID_ARG, "%s[%d]: shape too large", name, i);
   if (m.rows == 0 || m.cols == 0) return OUO_OK;
   if (!m.ptr) return set_error(OUO_ERR_INVALID_ARG, "%s[%d]: NULL pointer", name, i);
@@ -35,6 +35,15 @@ inline int validate_shape(const ouo_mat& m, int64_t rows, int64_t cols, const ch
   if (m.rows != rows || m.cols != cols)
     return set_error(OUO_ERR_INVALID_ARG, "%s[%d] is %lld x %lld, needs %lld x %lld", name, i,
                      (long long)m.rows, (long long)m.cols, (long long)rows, (long long)cols);
+  return OUO_OK;
+}
+
+// An output in place of an input has to be that input, element for element.
+inline int validate_in_place(const ouo_mat& out, int out_dtype, const ouo_mat& in, int in_dtype,
+                             const char* names) {
+  if (out.ptr == in.ptr && out.rows > 0 && out.cols > 0 &&
+      (out_dtype != in_dtype || (out.rows > 1 && out.ld != in.ld)))
+    return set_error(OUO_ERR_INVALID_ARG, "%s: in place needs the same type and row pitch", names);
   return OUO_OK;
 }
 

@@ -96,7 +96,7 @@ def test_quantize(dtype, transpose, layout):
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("rows,cols,pad,off", [
     (2048, 1024, 0, 0), (1100, 2049, 0, 0), (4097, 1000, 8, 0), (300, 9000, 3, 1),
-    (20001, 130, 6, 0), (60, 40000, 0, 0)])
+    (20001, 130, 6, 0), (60, 40000, 0, 0), (40000, 5, 0, 0), (30000, 32, 0, 0)])
 def test_quantize_large_transposed(rows, cols, pad, off, dtype):
     x = torch.randn((rows, cols), generator=_rng(rows), device=DEV)
     x[rows // 2] *= 30
@@ -167,7 +167,10 @@ def _check_mm(d, a, sa, b, sb):
 
 MM = [(1, 1, 1), (1, 128, 64), (3, 5, 33), (16, 16, 16), (17, 130, 257), (64, 300, 128),
       (129, 255, 1000), (1, 4096, 4096), (8, 1000, 4099), (33, 777, 515), (100, 2048, 1024),
-      (256, 256, 256), (300, 520, 384), (515, 1024, 129), (1030, 770, 640)]
+      (256, 256, 256), (300, 520, 384), (515, 1024, 129), (1030, 770, 640),
+      (2, 777, 515), (2, 5, 33), (1, 200, 131), (4, 1000, 2049), (40, 260, 2500),
+      (130, 40, 900), (2050, 20, 130), (1800, 2000, 200), (2100, 1700, 1111), (129, 12900, 64),
+      (12900, 130, 384)]
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
@@ -180,7 +183,8 @@ def test_matmul(m, n, k, dtype):
             a, b = pa.copy_(a), pb.copy_(b)
         sa = torch.rand(m, generator=_rng(3), device=DEV) + 0.1
         sb = torch.rand(n, generator=_rng(4), device=DEV) - 0.5
-        for pad, off in ((0, 0), (5, 1)):
+        # D on 16-byte boundaries (padded), or on none
+        for pad, off in ((-n % 8 + 8, 0), (5, 1)):
             d = Guard(m, n, dtype, pad, off)
             ouo.int8_matmul(a, sa, b, sb, d.v)
             _check_mm(d.v, a, sa, b, sb)

@@ -38,7 +38,7 @@ def _quant(lib, x=None, q=None, s=None, dt=L.OUO_BF16, t=0, n=1):
     (dict(t=1), b"needs 8 x 4"), (dict(t=2), b"transpose"), (dict(dt=2), b"dtype"),
     (dict(s=_v(None)), b"NULL"), (dict(s=_v(0x20002)), b"aligned"), (dict(n=-1), b"nmat"),
     (dict(n=4097), b"nmat"), (dict(x=_m(-1, 8)), b"negative"),
-    (dict(x=_m(1 << 31, 8), q=_m(1 << 31, 8)), b"large"),
+    (dict(x=_m((1 << 30) + 1, 8), q=_m((1 << 30) + 1, 8)), b"large"),
 ])
 def test_quantize_refuses(lib, kw, msg):
     assert _quant(lib, **kw) == BAD and msg in lib.ouo_last_error()
@@ -151,6 +151,17 @@ def test_distill_backward_refuses_what_is_not_in_place(lib):
     assert b"in place" in lib.ouo_last_error()
     assert call(_ref(s), 1, _ref(t), 0, _ref(t), 1.0, 0x100, 0x200, None, 1, None) == BAD
     assert call(_ref(s), 1, _ref(t), 0, _ref(t), 1.0, 0x100, None, _ref(s), 1, None) == BAD
+
+
+def test_in_place_needs_the_same_layout(lib):
+    x, wide = _m(4, 8), _m(4, 8, ld=16)
+    assert _rms(lib, x=x, h=wide) == BAD and b"H and X" in lib.ouo_last_error()
+    assert _rms(lib, x=x, h=x, hd=0) == BAD and b"H and X" in lib.ouo_last_error()
+    o = _m(4, 8, 0x90000)
+    assert _rms(lib, x=o, r=x, h=wide) == BAD and b"H and residual" in lib.ouo_last_error()
+    assert _rmsb(lib, dy=x, dx=wide) == BAD and b"dX and dY" in lib.ouo_last_error()
+    assert _rmsb(lib, dy=x, dx=x, dxd=0) == BAD and b"dX and dY" in lib.ouo_last_error()
+    assert _rmsb(lib, dy=o, dx=x, dh=wide) == BAD and b"dX and dH" in lib.ouo_last_error()
 
 
 def test_without_a_device(lib):
