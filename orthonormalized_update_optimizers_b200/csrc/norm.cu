@@ -30,8 +30,7 @@ __device__ __forceinline__ const char* row_of(const void* p, int64_t r, int64_t 
 }
 
 // A team per row, h in registers (as the values that H's type holds): x and
-// the residual are read once, and nothing is read back.  MODE 1 / 2: every
-// matrix and the weight bf16 / fp32, 16-byte accesses.
+// the residual are read once, and nothing is read back.
 template <int TPR, int NV, int MODE>
 __global__ void __launch_bounds__(kTeamThreads<TPR>) rms_kernel(const __grid_constant__ NormArgs a) {
   constexpr int kWarps = kTeamThreads<TPR> / 32, kTeams = kTeamThreads<TPR> / TPR;
@@ -40,8 +39,9 @@ __global__ void __launch_bounds__(kTeamThreads<TPR>) rms_kernel(const __grid_con
   const int64_t row = (int64_t)blockIdx.x * kTeams + (kTeams > 1 ? threadIdx.x / TPR : 0);
   if (kTeams > 1 && row >= a.rows) return;
   const int t = threadIdx.x % TPR, n = (int)a.cols;
-  const int xb = MODE ? MODE == 1 : a.x_bf16, hb = MODE ? MODE == 1 : a.h_bf16;
-  const int wb = MODE ? MODE == 1 : a.w_bf16, yb = MODE ? MODE == 1 : a.y_bf16;
+  constexpr int kBf = MODE == 1 || MODE == 3;
+  const int xb = MODE ? kBf : a.x_bf16, hb = MODE ? kBf : a.h_bf16;
+  const int wb = MODE ? kBf : a.w_bf16, yb = MODE ? kBf : a.y_bf16;
   RowRaw<TPR, NV, MODE> xr, rr;
   float v[NV][8];
   xr.load(row_of(a.X, row, a.ldx, xb), t, n, xb, a.vx);
@@ -68,7 +68,7 @@ __global__ void __launch_bounds__(kTeamThreads<TPR>) rms_kernel(const __grid_con
       }
     } else {
       store_row<TPR, NV, MODE>(h, t, n, hb, a.vh, v);
-      if (MODE == 0) {
+      if (MODE == 0 || MODE == 3) {
 #pragma unroll
         for (int c = 0; c < NV; ++c)
 #pragma unroll
@@ -103,9 +103,7 @@ __global__ void __launch_bounds__(kTeamThreads<TPR>) rms_kernel(const __grid_con
   if (!a.Q) return;
   const Quant q = quant_of(team_max<TPR>(__float_as_uint(m), redm));
   if (t == 0) a.scale[row] = q.scale;
-#pragma unroll
-  for (int c = 0; c < NV; ++c)
-    row_stq(a.Q + row * a.ldq, 8 * (t + c * TPR), n, a.vq, quant8(v[c], q));
+  store_q<TPR, NV, MODE>(a.Q + row * a.ldq, t, n, a.vq, v, q);
 }
 
 // Rows too long for registers: one block per row; h is read back (from H, or
@@ -176,8 +174,7 @@ struct NormBwdArgs {
 
 // A block of TPR threads takes rows b, b + grid, ...; every thread keeps the
 // same columns of all of them, so that its share of dw stays in registers
-// and leaves once, to row b of the partial sums.  MODE 1 / 2 (every matrix
-// bf16 / fp32, 16-byte accesses): DEPTH rows of dY, H and dH are on their way
+// and leaves once, to row b of the partial sums.  In modes 1 and 2 DEPTH rows of dY, H and dH are on their way
 // to shared memory (cp.async, to slots that only the copying warp reads, so
 // without block barriers), since the reduction of a row would otherwise leave the
 // memory idle.
@@ -187,15 +184,23 @@ __global__ void __launch_bounds__(TPR) rms_bwd_kernel(const __grid_constant__ No
   extern __shared__ __align__(16) uint4 ring[];  // [DEPTH][3][NV][TPR][kUnits]
   constexpr int kUnits = MODE == 2 ? 2 : 1;      // 16-byte pieces of a chunk
   const int t = threadIdx.x, n = (int)a.cols;
-  const int dyb = MODE ? MODE == 1 : a.dy_bf16, hb = MODE ? MODE == 1 : a.h_bf16;
-  const int dxb = MODE ? MODE == 1 : a.dx_bf16;
+  constexpr bool kRing = MODE == 1 || MODE == 2;
+  constexpr int kBf = MODE == 1 || MODE == 3;
+  const int dyb = MODE ? kBf : a.dy_bf16, hb = MODE ? kBf : a.h_bf16;
+  const int dxb = MODE ? kBf : a.dx_bf16;
   float w[NV][8], dw[NV][8];
+  if (MODE >= 3) {
+    RowRaw<TPR, NV, MODE> wr;
+    wr.load(a.W, t, n, kBf, 0);
+    wr.get(w);
+  } else {
 #pragma unroll
-  for (int c = 0; c < NV; ++c) {
-    row_ld8(a.W, 8 * (t + c * TPR), n, a.w_bf16, a.vw, w[c]);
+    for (int c = 0; c < NV; ++c) row_ld8(a.W, 8 * (t + c * TPR), n, a.w_bf16, a.vw, w[c]);
+  }
+#pragma unroll
+  for (int c = 0; c < NV; ++c)
 #pragma unroll
     for (int i = 0; i < 8; ++i) dw[c][i] = 0.f;
-  }
   const char* src[3] = {row_of(a.dY, blockIdx.x, a.lddy, dyb), row_of(a.H, blockIdx.x, a.ldh, hb),
                         a.dH ? row_of(a.dH, blockIdx.x, a.lddh, dxb) : nullptr};
   const int64_t step[3] = {a.lddy * (dyb ? 2 : 4) * gridDim.x, a.ldh * (hb ? 2 : 4) * gridDim.x,
@@ -222,17 +227,17 @@ __global__ void __launch_bounds__(TPR) rms_bwd_kernel(const __grid_constant__ No
     }
     ptx::copy16_commit();
   };
-  auto fetch = [&](RowRaw<TPR, NV, MODE>& r, int stage, int m) {
+  auto fetch = [&](auto& r, int stage, int m) {
 #pragma unroll
     for (int c = 0; c < NV; ++c) {
       const bool in = 8 * (t + c * TPR) < n;
       const uint4* q = ring + (((stage * 3 + m) * NV + c) * TPR + t) * kUnits;
       r.a[c] = in ? q[0] : make_uint4(0, 0, 0, 0);
-      if (MODE == 2) r.b[MODE == 1 ? 0 : c] = in ? q[kUnits - 1] : make_uint4(0, 0, 0, 0);
+      if constexpr (MODE == 2) r.b[c] = in ? q[kUnits - 1] : make_uint4(0, 0, 0, 0);
     }
   };
   int64_t ahead = blockIdx.x;
-  if (MODE) {
+  if constexpr (kRing) {
 #pragma unroll
     for (int s = 0; s < DEPTH; ++s, ahead += gridDim.x) issue(ahead, s);
   }
@@ -248,7 +253,7 @@ __global__ void __launch_bounds__(TPR) rms_bwd_kernel(const __grid_constant__ No
     RowRaw<TPR, NV, MODE> dr;
     {
       RowRaw<TPR, NV, MODE> gr, hr;
-      if (MODE) {
+      if constexpr (kRing) {
         asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 1) : "memory");
         if (MODE == 2) __syncwarp();
         fetch(gr, stage, 0);
@@ -285,7 +290,7 @@ __global__ void __launch_bounds__(TPR) rms_bwd_kernel(const __grid_constant__ No
 #pragma unroll
         for (int i = 0; i < 8; ++i) g[c][i] += h[c][i];
     }
-    if (MODE) {  // this stage's values are in registers
+    if constexpr (kRing) {  // this stage's values are in registers
       if (MODE == 2) __syncwarp();
       issue(ahead, stage);
       ahead += gridDim.x;
@@ -293,12 +298,16 @@ __global__ void __launch_bounds__(TPR) rms_bwd_kernel(const __grid_constant__ No
     }
     store_row<TPR, NV, MODE>(dx, t, n, dxb, a.vdx, g);
   }
-  if (MODE) ptx::copy16_wait_all();
+  if (kRing) ptx::copy16_wait_all();
   if (a.part) {
     float* part = a.part + blockIdx.x * a.cols;
+    if (MODE >= 3) {
+      store_row<TPR, NV, 4>(part, t, n, 0, 0, dw);
+    } else {
 #pragma unroll
-    for (int c = 0; c < NV; ++c)
-      row_st8(part, 8 * (t + c * TPR), n, 0, n % 4 == 0, dw[c]);
+      for (int c = 0; c < NV; ++c)
+        row_st8(part, 8 * (t + c * TPR), n, 0, n % 4 == 0, dw[c]);
+    }
   }
 }
 
@@ -353,7 +362,7 @@ rms_dw_kernel(const float* part, int nparts, int64_t cols, float* dw) {
 
 template <int TPR, int NV, int MODE, int DEPTH>
 int launch_bwd_as(const NormBwdArgs& a, unsigned grid, cudaStream_t s) {
-  constexpr size_t kSmem = MODE ? (size_t)DEPTH * 3 * NV * TPR * 16 * (MODE == 2 ? 2 : 1) : 0;
+  constexpr size_t kSmem = MODE == 1 || MODE == 2 ? (size_t)DEPTH * 3 * NV * TPR * 16 * (MODE == 2 ? 2 : 1) : 0;
   if (kSmem > 40 * 1024) {  // with the static part, past the default limit
     static Once once;
     OUO_TRY(once.smem(rms_bwd_kernel<TPR, NV, MODE, DEPTH>, kSmem));
@@ -369,6 +378,8 @@ int launch_bwd(const NormBwdArgs& a, unsigned grid, cudaStream_t s) {
   const int bf = a.dy_bf16 + a.h_bf16 + a.dx_bf16;
   if (vec && bf == 3) return launch_bwd_as<TPR, NV, 1, 4>(a, grid, s);
   if (vec && bf == 0) return launch_bwd_as<TPR, NV, 2, 2>(a, grid, s);
+  if (bf == 3 && a.w_bf16) return launch_bwd_as<TPR, NV, 3, 1>(a, grid, s);
+  if (bf == 0 && !a.w_bf16) return launch_bwd_as<TPR, NV, 4, 1>(a, grid, s);
   return launch_bwd_as<TPR, NV, 0, 1>(a, grid, s);
 }
 
@@ -446,15 +457,14 @@ int rms_norm(const ouo_mat* X, int x_dtype, const ouo_mat* residual, const ouo_m
     OUO_CHECK_LAUNCH();
     return OUO_OK;
   }
-  // one type throughout, and 16-byte accesses to all of it
   const bool vec = a.vx && a.vw && (!a.R || a.vr) && (!a.H || a.vh) && (!a.Y || a.vy) && n % 8 == 0;
   auto all = [&](int dt) {
-    return vec && x_dtype == dt && w_dtype == dt && (!H || h_dtype == dt) && (!Y || y_dtype == dt);
+    return x_dtype == dt && w_dtype == dt && (!H || h_dtype == dt) && (!Y || y_dtype == dt);
   };
-  const int fast = all(OUO_BF16) ? 1 : all(OUO_F32) ? 2 : 0;
-  return with_team(t, fast, [&](auto tpr, auto nv, auto mode) -> int {
+  const int mode = all(OUO_BF16) ? (vec ? 1 : 3) : all(OUO_F32) ? (vec ? 2 : 4) : 0;
+  return with_team(t, mode, [&](auto tpr, auto nv, auto md) -> int {
     constexpr int TPR = decltype(tpr)::value, NV = decltype(nv)::value;
-    constexpr int MODE = decltype(mode)::value;
+    constexpr int MODE = decltype(md)::value;
     constexpr int kTeams = kTeamThreads<TPR> / TPR;
     rms_kernel<TPR, NV, MODE><<<(unsigned)ceil_div(T, (int64_t)kTeams), kTeamThreads<TPR>, 0, s>>>(a);
     OUO_CHECK_LAUNCH();

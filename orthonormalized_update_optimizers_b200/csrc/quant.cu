@@ -59,8 +59,7 @@ quant_rows_kernel(const __grid_constant__ QuantArgs a) {
   const Quant q = quant_of(team_max<TPR>(__float_as_uint(m), red));
   if (t == 0) a.scale[g][r] = q.scale;
   int8_t* o = a.Q[g] + r * a.ldq[g];
-#pragma unroll
-  for (int c = 0; c < NV; ++c) row_stq(o, 8 * (t + c * TPR), n, a.vecq[g], quant8(v[c], q));
+  store_q<TPR, NV, MODE>(o, t, n, a.vecq[g], v, q);
 }
 
 // Rows too long for registers: one block per row, read twice (the second
@@ -609,18 +608,18 @@ extern "C" int quantize_int8(const ouo_mat* X, int x_dtype, const ouo_mat* Q, fl
     a.row_start[cn] = acc;
     if (acc == 0) continue;
     if (acc > 0x7fffffff) return set_error(OUO_ERR_UNSUPPORTED, "X: too many rows in one batch");
-    int fast = bf16 ? 1 : 2;
+    int mode = bf16 ? 1 : 2;
     for (int i = 0; i < cn; ++i)
-      if (!a.vecx[i] || a.cols[i] % 8 != 0) fast = 0;
+      if (!a.vecx[i] || a.cols[i] % 8 != 0) mode = bf16 ? 3 : 4;
     const Team t = team_for(acc, longest);
     if (t.tpr == 0) {
       quant_long_kernel<<<(unsigned)acc, 512, 0, s>>>(a);
       OUO_CHECK_LAUNCH();
       continue;
     }
-    OUO_TRY(with_team(t, fast, [&](auto tpr, auto nv, auto mode) -> int {
+    OUO_TRY(with_team(t, mode, [&](auto tpr, auto nv, auto md) -> int {
       constexpr int TPR = decltype(tpr)::value, NV = decltype(nv)::value;
-      constexpr int MODE = decltype(mode)::value;
+      constexpr int MODE = decltype(md)::value;
       constexpr int kTeams = kTeamThreads<TPR> / TPR;
       quant_rows_kernel<TPR, NV, MODE><<<(unsigned)ceil_div(acc, (int64_t)kTeams), kTeamThreads<TPR>, 0, s>>>(a);
       OUO_CHECK_LAUNCH();

@@ -223,21 +223,19 @@ __device__ __forceinline__ void row_st8(void* p, int j, int n, int bf16, int vec
   }
 }
 
-// A thread's chunks of one row, as they are stored.  Loading and converting
+// A thread's share of one row: NV chunks of 8 elements.  Loading and converting
 // are separate, so that every load of the row is in flight before the first
-// one is waited for.  MODE 1: bf16, 2: fp32, both with 16-byte accesses and n
-// a multiple of 8, known when the kernel is compiled; 0: any type, alignment
-// and n (element by element, kept as fp32).
+// one is waited for.  The mode says, when the kernel is compiled, what the
+// matrices are:
+//   1, 2: all bf16 / fp32, 16-byte accesses, n a multiple of 8: chunk c of
+//         thread t is elements 8 (t + c TPR) .. + 7;
+//   3, 4: all bf16 / fp32, any alignment and n: element i of chunk c is
+//         (8 c + i) TPR + t, so that a warp's accesses lie next to each other;
+//   0:    mixed types: as 1 and 2, element by element where need be.
 template <int TPR, int NV, int MODE>
 struct RowRaw {
-  uint4 a[NV], b[MODE == 1 ? 1 : NV];  // b: the second half of fp32 chunks
-
-  __device__ __forceinline__ void set(int c, const float v[8]) {
-    a[c] = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
-                      __float_as_uint(v[3]));
-    b[MODE == 1 ? 0 : c] = make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]),
-                                      __float_as_uint(v[6]), __float_as_uint(v[7]));
-  }
+  uint4 a[MODE <= 2 ? NV : 1], b[MODE == 0 || MODE == 2 ? NV : 1];  // b: second half of fp32
+  float f[MODE >= 3 ? NV : 1][8];
 
   __device__ __forceinline__ void load(const void* p, int t, int n, int bf16, int vec) {
     const uint4 zero = make_uint4(0, 0, 0, 0);
@@ -245,15 +243,24 @@ struct RowRaw {
 #pragma unroll
     for (int c = 0; c < NV; ++c) {
       const int i = t + c * TPR;
-      if (MODE == 1) {
+      if constexpr (MODE == 1) {
         a[c] = 8 * i < n ? q[i] : zero;
-      } else if (MODE == 2) {
+      } else if constexpr (MODE == 2) {
         a[c] = 8 * i < n ? q[2 * i] : zero;
         b[c] = 8 * i < n ? q[2 * i + 1] : zero;
+      } else if constexpr (MODE >= 3) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int j = (8 * c + e) * TPR + t;
+          f[c][e] = j < n ? ld1(p, j, MODE == 3) : 0.f;
+        }
       } else {
         float v[8];
         row_ld8(p, 8 * i, n, bf16, vec, v);
-        set(c, v);
+        a[c] = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                          __float_as_uint(v[3]));
+        b[c] = make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]),
+                          __float_as_uint(v[7]));
       }
     }
   }
@@ -261,8 +268,11 @@ struct RowRaw {
   __device__ __forceinline__ void get(float v[NV][8]) const {
 #pragma unroll
     for (int c = 0; c < NV; ++c) {
-      if (MODE == 1) {
+      if constexpr (MODE == 1) {
         unpack8(a[c], v[c]);
+      } else if constexpr (MODE >= 3) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[c][e] = f[c][e];
       } else {
         const uint4 x = a[c], y = b[c];
         v[c][0] = __uint_as_float(x.x); v[c][1] = __uint_as_float(x.y);
@@ -280,8 +290,17 @@ __device__ __forceinline__ void store_row(void* p, int t, int n, int bf16, int v
 #pragma unroll
   for (int c = 0; c < NV; ++c) {
     const int j = 8 * (t + c * TPR);
-    if (MODE == 0) row_st8(p, j, n, bf16, vec, v[c]);
-    else if (j < n) st8(p, j, MODE == 1, v[c]);
+    if (MODE >= 3) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int k = (8 * c + e) * TPR + t;
+        if (k < n) st1(p, k, v[c][e], MODE == 3);
+      }
+    } else if (MODE == 0) {
+      row_st8(p, j, n, bf16, vec, v[c]);
+    } else if (j < n) {
+      st8(p, j, MODE == 1, v[c]);
+    }
   }
 }
 
@@ -327,7 +346,13 @@ int with_team_of(Team t, F&& f) {
 template <class F>
 int with_team(Team t, int mode, F&& f) {
   return with_team_of(t, [&](auto tpr, auto nv) -> int {
-    return mode == 1 ? f(tpr, nv, C<1>{}) : mode == 2 ? f(tpr, nv, C<2>{}) : f(tpr, nv, C<0>{});
+    switch (mode) {
+      case 1: return f(tpr, nv, C<1>{});
+      case 2: return f(tpr, nv, C<2>{});
+      case 3: return f(tpr, nv, C<3>{});
+      case 4: return f(tpr, nv, C<4>{});
+      default: return f(tpr, nv, C<0>{});
+    }
   });
 }
 
@@ -393,6 +418,25 @@ __device__ __forceinline__ void row_stq(int8_t* p, int j, int n, int vec, uint2 
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       if (j + i < n) p[j + i] = (int8_t)((i < 4 ? v.x >> (8 * i) : v.y >> (8 * (i - 4))) & 255u);
+  }
+}
+
+// A thread's share of a row in 8 bits.
+template <int TPR, int NV, int MODE>
+__device__ __forceinline__ void store_q(int8_t* p, int t, int n, int vec, const float v[NV][8],
+                                        const Quant& q) {
+#pragma unroll
+  for (int c = 0; c < NV; ++c) {
+    const uint2 o = quant8(v[c], q);
+    if (MODE >= 3) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int k = (8 * c + e) * TPR + t;
+        if (k < n) p[k] = (int8_t)((e < 4 ? o.x >> (8 * e) : o.y >> (8 * (e - 4))) & 255u);
+      }
+    } else {
+      row_stq(p, 8 * (t + c * TPR), n, vec, o);
+    }
   }
 }
 
