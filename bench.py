@@ -58,15 +58,18 @@ def _args():
     ap.add_argument("--no-sweep", action="store_true",
                     help="skip the standard-vs-Gram crossover points of the JSON line")
     ap.add_argument("--cpu-sample-layers", type=int, default=1)
-    ap.add_argument("--micro", choices=["gram", "dion", "dion_set"], default=None,
+    ap.add_argument("--micro", choices=["gram", "dion", "dion_set", "head8"], default=None,
                     help="one kernel-level case for profiling: Gram NS on --nb blocks "
                          "of --m x --n bf16, one Dion / Orth-Dion matrix --m x --n "
-                         "at --rank (--mode colnorm|qr), or the 8B-shaped set of "
-                         "--layers layers in one grouped Dion / Orth-Dion call")
+                         "at --rank (--mode colnorm|qr), the 8B-shaped set of "
+                         "--layers layers in one grouped Dion / Orth-Dion call, or "
+                         "one training step of an 8-bit --m x --n head on --tokens "
+                         "tokens against a teacher, Dion3 step included")
     ap.add_argument("--nb", type=int, default=32)
     ap.add_argument("--m", type=int, default=1792)
     ap.add_argument("--n", type=int, default=4096)
     ap.add_argument("--rank", type=int, default=256)
+    ap.add_argument("--tokens", type=int, default=4096)
     ap.add_argument("--mode", choices=["colnorm", "qr"], default="qr")
     ap.add_argument("--sweep", action="store_true",
                     help="shape sweep instead of the step: standard vs Gram NS over "
@@ -904,6 +907,61 @@ def run_sweep(args):
                       "ns": ns_rows, "dion": dion_rows, "clocks": clocks}), flush=True)
 
 
+def head8_step(tokens, m, n, dev, k=32):
+    """One training step of an 8-bit m x n head against a teacher: norm with
+    the residual's addition, product, distillation loss, the gradients, and
+    the weight through the Dion3 step to its 8-bit copies again.  Returns the
+    step and its integer operations."""
+    import torch
+
+    import orthonormalized_update_optimizers_b200 as ouo
+    from orthonormalized_update_optimizers_b200 import synth
+
+    bf, f32 = torch.bfloat16, torch.float32
+    e = lambda *s, d=f32: torch.empty(s, dtype=d, device=dev)  # noqa: E731
+    q = lambda r, c: (ouo.int8_empty(r, c, dev), e(r))  # noqa: E731
+    X = synth.gaussian((tokens, n), synth.seed_for(5, 0), 1.0, bf, dev)
+    R = synth.gaussian((tokens, n), synth.seed_for(5, 1), 1.0, bf, dev)
+    W = synth.gaussian((m, n), synth.seed_for(5, 2), 0.02, bf, dev)
+    g = torch.ones(n, dtype=bf, device=dev)
+    teacher = synth.gaussian((tokens, k), synth.seed_for(5, 3), 2.0, f32, dev)
+    idx = ((torch.arange(tokens, device=dev)[:, None] * 7919
+            + torch.arange(k, device=dev) * max(1, m // k)) % m).to(torch.int32)
+    dloss = torch.full((tokens,), 1.0 / tokens, device=dev)
+    H, Y, rstd = e(tokens, n, d=bf), e(tokens, n, d=bf), e(tokens)
+    S, dS = e(tokens, m, d=bf), e(tokens, m, d=bf)
+    loss, lse, dY, dX, dg = e(tokens), e(tokens), e(tokens, n, d=bf), e(tokens, n, d=bf), e(n)
+    G, M, keys = e(m, n), torch.zeros((m, n), device=dev), e(m, d=torch.float64)
+    yq, yt, wq, wt = q(tokens, n), q(n, tokens), q(m, n), q(n, m)
+    dq, dt = q(tokens, m), q(m, tokens)
+    kept = ouo.dion3_num_selected(m, RHO)
+    sel, X0, sc = e(kept, d=torch.int32), ouo.batch_empty([(kept, n)], bf, dev), e(1)
+    O = [torch.empty_like(X0[0])]
+    ns = ouo.ns_params(normalize=False)
+    ws = torch.empty(ouo.gram_ns_workspace_bytes(X0, ns), dtype=torch.uint8, device=dev)
+    ouo.quantize_int8(W, *wq)
+    ouo.quantize_int8(W, *wt, transpose=True)
+
+    def step():
+        ouo.rms_norm(X, g, Y=Y, Q=yq[0], scale=yq[1], residual=R, H=H, rstd=rstd)
+        ouo.int8_matmul(*yq, *wq, S)
+        ouo.distill_loss(S, teacher, idx, loss, lse)
+        ouo.distill_loss_backward(S, teacher, idx, lse, dloss, dS)
+        ouo.quantize_int8(dS, *dq)
+        ouo.quantize_int8([dS, Y], [dt[0], yt[0]], [dt[1], yt[1]], transpose=True)
+        ouo.int8_matmul(*dq, *wt, dY)
+        ouo.int8_matmul(*dt, *yt, G)
+        ouo.rms_norm_backward(dY, H, g, rstd, dX, dweight=dg)
+        ouo.dion_momentum_update([M], [G], 0.95, "accum", keys)
+        ouo.dion3_select_rows([M], keys, RHO, sel, X0, sc)
+        ouo.gram_ns_orthogonalize(X0, O, ns, workspace=ws)
+        ouo.apply_update([W], O, lr=0.02, idx=sel)
+        ouo.quantize_int8(W, *wq)
+        ouo.quantize_int8(W, *wt, transpose=True)
+
+    return step, 6 * tokens * m * n
+
+
 def run_micro(args):
     """One kernel-level case (for ncu captures): W warm-up calls, then K
     calls timed with CUDA events; prints one JSON line."""
@@ -924,6 +982,9 @@ def run_micro(args):
         fn = lambda: ouo.gram_ns_orthogonalize(Xb, Ob, p, workspace=ws)  # noqa: E731
         flops = args.nb * sum(gram_ns_flops(m, n))
         case = f"Gram NS, {args.nb} x bf16 {m}x{n}"
+    elif args.micro == "head8":
+        fn, flops = head8_step(args.tokens, m, n, dev)
+        case = f"8-bit head {m}x{n}, {args.tokens} tokens, distillation and Dion3 step"
     elif args.micro == "dion_set":
         r = args.rank
         shapes = [(a, b) for _, a, b in synth.llama8b_shapes(args.layers)]
