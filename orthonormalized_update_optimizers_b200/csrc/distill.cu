@@ -161,6 +161,29 @@ distill_kernel(const __grid_constant__ DistillArgs a) {
   asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(nct));
   const uint32_t rank = nct > 1 ? ptx::cluster_ctarank() : 0u;
   const int64_t row = blockIdx.x / nct;
+  const char* s = reinterpret_cast<const char*>(a.S) + row * a.lds * (BF ? 2 : 4);
+  const int64_t per = (a.V + nct - 1) / nct;
+  const int64_t j0 = rank * per < a.V ? rank * per : a.V;
+  const int64_t j1 = j0 + per < a.V ? j0 + per : a.V;
+  const Run r = split_run(s, BF ? 2 : 4, j0, j1);
+  const float c = a.inv_tau * kLog2e;
+  Soft f{kLowest, 0.f};
+  int64_t j = r.ja + 8 * threadIdx.x;
+  // kU chunks at a time, the next ones on their way while these are summed (the
+  // first ones while the teacher's entries are)
+  constexpr int kN = kU * (BF ? 1 : 2);
+  constexpr int64_t kStep = (int64_t)8 * kDThreads * kU;
+  auto fetch = [&](uint4 (&raw)[kN], int64_t at) {
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const uint4* p = reinterpret_cast<const uint4*>(s + (at + 8 * kDThreads * u) * (BF ? 2 : 4));
+#pragma unroll
+      for (int h = 0; h < kN / kU; ++h) raw[u * (kN / kU) + h] = __ldcs(p + h);
+    }
+  };
+  auto whole = [&](int64_t at) { return at + 8 * kDThreads * (kU - 1) < r.jb; };
+  uint4 cur[kN];
+  if (whole(j)) fetch(cur, j);
   const bool any = teacher_probs(a, row, t, red);  // the same in every CTA of the cluster
   if (!any) {
     if (threadIdx.x == 0 && rank == 0) {
@@ -169,34 +192,20 @@ distill_kernel(const __grid_constant__ DistillArgs a) {
     }
     return;
   }
-  const char* s = reinterpret_cast<const char*>(a.S) + row * a.lds * (BF ? 2 : 4);
-  const int64_t per = (a.V + nct - 1) / nct;
-  const int64_t j0 = rank * per < a.V ? rank * per : a.V;
-  const int64_t j1 = j0 + per < a.V ? j0 + per : a.V;
-  const Run r = split_run(s, BF ? 2 : 4, j0, j1);
-  const float c = a.inv_tau * kLog2e;
-  Soft f{kLowest, 0.f};
+  // the logit of the thread's first entry, needed last
+  float at_entry = 0.f;
+  if (threadIdx.x < a.K && t.idx[threadIdx.x] >= 0) at_entry = ld1(s, t.idx[threadIdx.x], BF);
   if (j0 + threadIdx.x < r.ja) f.add1(ld1(s, j0 + threadIdx.x, BF), c);
-  int64_t j = r.ja + 8 * threadIdx.x;
-  for (; j + 8 * kDThreads * (kU - 1) < r.jb; j += 8 * kDThreads * kU) {
-    uint4 raw[kU * (BF ? 1 : 2)];
-#pragma unroll
-    for (int u = 0; u < kU; ++u) {
-      const uint4* p = reinterpret_cast<const uint4*>(s + (j + 8 * kDThreads * u) * (BF ? 2 : 4));
-      if (BF) {
-        raw[u] = __ldcs(p);
-      } else {
-        raw[2 * u] = __ldcs(p);
-        raw[2 * u + 1] = __ldcs(p + 1);
-      }
-    }
+  while (whole(j)) {
+    uint4 next[kN];
+    if (whole(j + kStep)) fetch(next, j + kStep);
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
       float v[8];
       if (BF) {
-        unpack8(raw[u], v);
+        unpack8(cur[u], v);
       } else {
-        const uint4 x = raw[2 * u], y = raw[2 * u + 1];
+        const uint4 x = cur[u * (kN / kU)], y = cur[u * (kN / kU) + kN / kU - 1];
         v[0] = __uint_as_float(x.x); v[1] = __uint_as_float(x.y);
         v[2] = __uint_as_float(x.z); v[3] = __uint_as_float(x.w);
         v[4] = __uint_as_float(y.x); v[5] = __uint_as_float(y.y);
@@ -204,6 +213,9 @@ distill_kernel(const __grid_constant__ DistillArgs a) {
       }
       f.add(v, c);
     }
+#pragma unroll
+    for (int i = 0; i < kN; ++i) cur[i] = next[i];
+    j += kStep;
   }
   for (; j < r.jb; j += 8 * kDThreads) {
     float v[8];
@@ -248,7 +260,8 @@ distill_kernel(const __grid_constant__ DistillArgs a) {
     const int i = t.idx[k];
     const float p = t.p[k];
     if (i < 0 || p == 0.f) continue;  // p = 0 also where the student's logit is -inf
-    acc += (double)p * ((double)t.lp[k] - ((double)(ld1(s, i, BF) * a.inv_tau) - lse));
+    const float x = k == threadIdx.x ? at_entry : ld1(s, i, BF);
+    acc += (double)p * ((double)t.lp[k] - ((double)(x * a.inv_tau) - lse));
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
