@@ -76,19 +76,21 @@ s8_simt_kernel(const int8_t* A, int64_t lda, const int8_t* B, int64_t ldb, const
 }
 
 
-// MT tokens, one or two: a warp per 2 or 4 rows of B, 16 bytes a lane and load,
+// MT tokens, one or two: a warp per row of B (per 4 for two
+// tokens), 16 bytes a lane and load,
 // dp4a.  Bound by reading B; the tensor-core kernels' set-up (TMEM, barriers,
 // a pipeline to fill) costs more than these few products.
+constexpr int kVecThreads = 128;
 template <int MT>
-constexpr int kVecRows = MT == 1 ? 2 : 4;
+constexpr int kVecRows = MT == 1 ? 1 : 4;
 
 template <int MT>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(kVecThreads)
 s8_vec_kernel(const int8_t* A, int64_t lda, const int8_t* B, int64_t ldb, const float* as,
               const float* bs, void* D, int64_t ldd, int bf16, int N, int K) {
   constexpr int kR = kVecRows<MT>;
   const int lane = threadIdx.x & 31;
-  const int64_t n0 = ((int64_t)blockIdx.x * 8 + (threadIdx.x >> 5)) * kR;
+  const int64_t n0 = ((int64_t)blockIdx.x * (kVecThreads / 32) + (threadIdx.x >> 5)) * kR;
   if (n0 >= N) return;
   const int8_t* b[kR];
 #pragma unroll
@@ -838,9 +840,9 @@ int run_simt(const Product& p, cudaStream_t s) {
 
 template <int MT>
 int run_vec(const Product& p, cudaStream_t s) {
-  const int64_t blocks = ceil_div(p.D.cols, (int64_t)8 * kVecRows<MT>);
+  const int64_t blocks = ceil_div(p.D.cols, (int64_t)(kVecThreads / 32) * kVecRows<MT>);
   if (blocks > 0x7fffffff) return set_error(OUO_ERR_UNSUPPORTED, "D: too many columns");
-  s8_vec_kernel<MT><<<(unsigned)blocks, 256, 0, s>>>(
+  s8_vec_kernel<MT><<<(unsigned)blocks, kVecThreads, 0, s>>>(
       (const int8_t*)p.A.ptr, p.A.ld, (const int8_t*)p.B.ptr, p.B.ld, p.as, p.bs, p.D.ptr, p.D.ld,
       p.bf16, (int)p.D.cols, (int)p.A.cols);
   OUO_CHECK_LAUNCH();
