@@ -76,9 +76,8 @@ s8_simt_kernel(const int8_t* A, int64_t lda, const int8_t* B, int64_t ldb, const
 }
 
 
-// MT tokens, one or two: a warp per row of B (per 4 for two
-// tokens), 16 bytes a lane and load,
-// dp4a.  Bound by reading B; the tensor-core kernels' set-up (TMEM, barriers,
+// MT tokens, one or two: a warp per row of B (per 4 for two tokens), 16 bytes a
+// lane and load, dp4a.  Bound by reading B; the tensor-core kernels' set-up (TMEM, barriers,
 // a pipeline to fill) costs more than these few products.
 constexpr int kVecThreads = 128;
 template <int MT>
@@ -474,6 +473,12 @@ s8_split_kernel(const __grid_constant__ SplitArgs a) {
   const int r0 = tile / a.tiles_t * 128, t0 = tile % a.tiles_t * BN;
   const int kb0 = (int)rank * a.nk_cta, kb1 = min(a.nk, kb0 + a.nk_cta);
 
+  auto load = [&](int stage, int kb) {
+    ptx::mbar_arrive_expect_tx(&full[stage], C::kStage);
+    uint8_t* s = smem + stage * C::kStage;
+    ptx::tma_load_2d(s, &a.tmR, &full[stage], kb * (int)kRowB, r0);
+    ptx::tma_load_2d(s + kABytes, &a.tmT, &full[stage], kb * (int)kRowB, t0);
+  };
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
       ptx::mbar_init(&full[s], 1);
@@ -482,8 +487,9 @@ s8_split_kernel(const __grid_constant__ SplitArgs a) {
     ptx::mbar_init(done, 1);
     *abort_flag = 0;
     ptx::fence_barrier_init();
-    ptx::prefetch_tmap(&a.tmR);
-    ptx::prefetch_tmap(&a.tmT);
+    ptx::fence_async_shared();  // the barriers, for the TMA
+    // the first stages' loads need nobody else: they run under the set-up
+    for (int i = 0; i < C::kStages && kb0 + i < kb1; ++i) load(i, kb0 + i);
   }
   if (warp == 1) {
     ptx::tmem_alloc(holder, C::kTmemCols);
@@ -503,18 +509,16 @@ s8_split_kernel(const __grid_constant__ SplitArgs a) {
   __syncwarp();
 
   if (warp == 0 && lane == 0) {
+    // stages are refilled in order, as their products finish
     uint32_t stage = 0, phase = 0;
-    int issued = 0;
+    int issued = min(C::kStages, max(0, kb1 - kb0));
     bool ok = true;
-    for (int kb = kb0; kb < kb1; ++kb) {
-      if (!ptx::mbar_wait(&empty[stage], phase ^ 1, abort_flag)) {
+    for (int kb = kb0 + C::kStages; kb < kb1; ++kb) {
+      if (!ptx::mbar_wait(&empty[stage], phase, abort_flag)) {
         ok = false;
         break;
       }
-      ptx::mbar_arrive_expect_tx(&full[stage], C::kStage);
-      uint8_t* s = smem + stage * C::kStage;
-      ptx::tma_load_2d(s, &a.tmR, &full[stage], kb * (int)kRowB, r0);
-      ptx::tma_load_2d(s + kABytes, &a.tmT, &full[stage], kb * (int)kRowB, t0);
+      load((int)stage, kb);
       ++issued;
       if (++stage == (uint32_t)C::kStages) { stage = 0; phase ^= 1; }
     }
