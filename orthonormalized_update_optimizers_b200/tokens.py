@@ -58,9 +58,10 @@ def _mat(t: torch.Tensor, name: str, dev: int, dtype: Optional[torch.dtype] = No
     already looked up by _code)."""
     if dtype is not None and t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != 2:
+    shape = t.shape
+    if len(shape) != 2:
         raise ValueError(f"{name} must be 2-D")
-    r, c = t.shape
+    r, c = shape
     ld, one = t.stride()
     if one != 1 and c > 1:
         raise ValueError(f"{name} needs unit column stride")
@@ -88,8 +89,6 @@ def _vec(t: torch.Tensor, name: str, dev: int, n: int,
 
 
 def _mats(ts, name: str, dev: int, dtype: Optional[torch.dtype] = None) -> bytes:
-    if len(ts) == 1:
-        return _mat(ts[0], name, dev, dtype)
     for t in ts:
         if t.dtype is not ts[0].dtype:
             raise TypeError(f"{name}: a batch must have one dtype")
@@ -104,6 +103,15 @@ def _vecs(x: Tensors, name: str, dev: int, owners) -> bytes:
     return b"".join([_ptr_bytes(_vec(t, name, dev, m.shape[0])) for t, m in zip(ts, owners)])
 
 
+def _scale(t: torch.Tensor, name: str, dev: int, rows: int) -> bytes:
+    """_vecs of a single matrix."""
+    if not isinstance(t, torch.Tensor):
+        if len(t) != 1:
+            raise ValueError(f"{name} needs one vector per matrix")
+        t = t[0]
+    return _ptr_bytes(_vec(t, name, dev, rows))
+
+
 def _workspace(need: int, given: Optional[torch.Tensor], dev: int, stream):
     """(address, bytes) of a workspace: the caller's, or one allocated here
     (the allocator keeps it for the stream that uses it)."""
@@ -116,17 +124,23 @@ def _workspace(need: int, given: Optional[torch.Tensor], dev: int, stream):
     return _vec(given, "workspace", dev, need, torch.uint8), given.numel()
 
 
+_get_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_entry = {}
+
+
 def _run(fname: str, dev: int, stream, *args) -> None:
     """Calls the library with the tensors' device current (the first one's,
     which every other was compared with), the stream last."""
+    fn = _entry.get(fname)
+    if fn is None:
+        fn = _entry[fname] = getattr(L.lib(), fname)
     if stream is None:
         s = _raw_stream(dev)
     else:
         if stream.device.index != dev:
             raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{dev}")
         s = stream.cuda_stream
-    fn = getattr(L.lib(), fname)
-    if torch.cuda.current_device() == dev:
+    if _get_device() == dev:
         rc = fn(*args, s)
     else:
         with torch.cuda.device(dev):
@@ -164,20 +178,25 @@ def quantize_int8(X: Tensors, Q: Tensors, scale: Tensors, transpose: bool = Fals
     X's transpose (one scale per column of X).  X, Q and scale are tensors, or
     lists of equal length.  Large transposed matrices take a workspace
     (allocated here unless given)."""
-    xs, qs = _list(X), _list(Q)
-    n = len(xs)
-    if len(qs) != n:
-        raise ValueError(f"X has {n} matrices, Q {len(qs)}")
-    if n == 0:
-        return
-    dev, code = xs[0].get_device(), _code(xs[0], "X")
-    x = _mats(xs, "X", dev)
+    if isinstance(X, torch.Tensor) and isinstance(Q, torch.Tensor):
+        dev, code, n = X.get_device(), _code(X, "X"), 1
+        x, q = _mat(X, "X", dev), _mat(Q, "Q", dev, torch.int8)
+        sc = _scale(scale, "scale", dev, Q.shape[0])
+    else:
+        xs, qs = _list(X), _list(Q)
+        n = len(xs)
+        if len(qs) != n:
+            raise ValueError(f"X has {n} matrices, Q {len(qs)}")
+        if n == 0:
+            return
+        dev, code = xs[0].get_device(), _code(xs[0], "X")
+        x, q = _mats(xs, "X", dev), _mats(qs, "Q", dev, torch.int8)
+        sc = _vecs(scale, "scale", dev, qs)
     wp, wn = None, 0
     if transpose:
         wp, wn = _workspace(L.lib().quantize_int8_workspace_bytes(x, code, n, 1), workspace, dev,
                             stream)
-    _run("quantize_int8", dev, stream, x, code, _mats(qs, "Q", dev, torch.int8),
-         _vecs(scale, "scale", dev, qs), n, 1 if transpose else 0, wp, wn)
+    _run("quantize_int8", dev, stream, x, code, q, sc, n, 1 if transpose else 0, wp, wn)
 
 
 def int8_matmul(A: Tensors, a_scale: Tensors, B: Tensors, b_scale: Tensors, D: Tensors,
@@ -185,17 +204,25 @@ def int8_matmul(A: Tensors, a_scale: Tensors, B: Tensors, b_scale: Tensors, D: T
     """D <- diag(a_scale) (A B^T) diag(b_scale), A (M x K) and B (N x K) 8-bit
     integers as quantize_int8 writes them.  Tensors, or lists of equal
     length."""
-    As, Bs, Ds = _list(A), _list(B), _list(D)
-    n = len(As)
-    if len(Bs) != n or len(Ds) != n:
-        raise ValueError(f"A has {n} matrices, B {len(Bs)}, D {len(Ds)}")
-    if n == 0:
-        return
-    dev = As[0].get_device()
-    a, b = _mats(As, "A", dev, torch.int8), _mats(Bs, "B", dev, torch.int8)
+    if isinstance(A, torch.Tensor) and isinstance(B, torch.Tensor) and isinstance(D, torch.Tensor):
+        dev, n = A.get_device(), 1
+        a, b = _mat(A, "A", dev, torch.int8), _mat(B, "B", dev, torch.int8)
+        d, code = _mat(D, "D", dev), _code(D, "D")
+        sa = _scale(a_scale, "a_scale", dev, A.shape[0])
+        sb = _scale(b_scale, "b_scale", dev, B.shape[0])
+    else:
+        As, Bs, Ds = _list(A), _list(B), _list(D)
+        n = len(As)
+        if len(Bs) != n or len(Ds) != n:
+            raise ValueError(f"A has {n} matrices, B {len(Bs)}, D {len(Ds)}")
+        if n == 0:
+            return
+        dev = As[0].get_device()
+        a, b = _mats(As, "A", dev, torch.int8), _mats(Bs, "B", dev, torch.int8)
+        d, code = _mats(Ds, "D", dev), _code(Ds[0], "D")
+        sa, sb = _vecs(a_scale, "a_scale", dev, As), _vecs(b_scale, "b_scale", dev, Bs)
     st = None if status is None else _vec(status, "status", dev, 1, torch.int32)
-    _run("int8_matmul", dev, stream, a, _vecs(a_scale, "a_scale", dev, As), b,
-         _vecs(b_scale, "b_scale", dev, Bs), _mats(Ds, "D", dev), _code(Ds[0], "D"), n, st)
+    _run("int8_matmul", dev, stream, a, sa, b, sb, d, code, n, st)
 
 
 def rms_norm(X: torch.Tensor, weight: torch.Tensor, Y: Optional[torch.Tensor] = None,
