@@ -454,17 +454,17 @@ int rms_norm(const ouo_mat* X, int x_dtype, const ouo_mat* residual, const ouo_m
   a.vy = Y ? rows16(*Y, elem_size(y_dtype)) : 0;
   a.vq = Q ? (uintptr_t)a.Q % 8 == 0 && (T <= 1 || a.ldq % 8 == 0) : 0;
   cudaStream_t s = (cudaStream_t)stream;
-  const Team t = team_for(T, n);
-  if (t.tpr == 0) {
-    rms_long_kernel<<<(unsigned)T, 512, 0, s>>>(a);
-    OUO_CHECK_LAUNCH();
-    return OUO_OK;
-  }
   const bool vec = a.vx && a.vw && (!a.R || a.vr) && (!a.H || a.vh) && (!a.Y || a.vy) && n % 8 == 0;
   auto all = [&](int dt) {
     return x_dtype == dt && w_dtype == dt && (!H || h_dtype == dt) && (!Y || y_dtype == dt);
   };
   const int mode = all(OUO_BF16) ? (vec ? 1 : 3) : all(OUO_F32) ? (vec ? 2 : 4) : 0;
+  const Team t = team_for(T, n, mode);
+  if (t.tpr == 0) {
+    rms_long_kernel<<<(unsigned)T, 512, 0, s>>>(a);
+    OUO_CHECK_LAUNCH();
+    return OUO_OK;
+  }
   return with_team(t, mode, [&](auto tpr, auto nv, auto md) -> int {
     constexpr int TPR = decltype(tpr)::value, NV = decltype(nv)::value;
     constexpr int MODE = decltype(md)::value;
@@ -530,7 +530,9 @@ int rms_norm_backward(const ouo_mat* dY, int dy_dtype, const ouo_mat* H, int h_d
     a.vdh = dH ? rows16(*dH, elem_size(dx_dtype)) : 0;
     a.vdx = rows16(*dX, elem_size(dx_dtype));
     const unsigned grid = (unsigned)parts;
+    const bool vec = a.vdy && a.vh && a.vdx && (a.vdh || !dH) && n % 8 == 0;
     if (n <= 128 * 8) OUO_TRY((launch_bwd<128, 1>(a, grid, s)));
+    else if (n <= 512 * 8 && !vec) OUO_TRY((launch_bwd<512, 1>(a, grid, s)));
     else if (n <= 128 * 16) OUO_TRY((launch_bwd<128, 2>(a, grid, s)));
     else if (n <= 256 * 16) OUO_TRY((launch_bwd<256, 2>(a, grid, s)));
     else if (n <= 512 * 16) OUO_TRY((launch_bwd<512, 2>(a, grid, s)));

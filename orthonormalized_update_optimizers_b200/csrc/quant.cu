@@ -47,6 +47,11 @@ quant_rows_kernel(const __grid_constant__ QuantArgs a) {
   const int g = matrix_of(a, row);
   const int64_t r = row - a.row_start[g];
   const int n = (int)a.cols[g];
+  if (n == 0) {  // rows without columns: nothing to read (the team's row, so no
+                 // thread waits for it)
+    if (t == 0) a.scale[g][r] = 0.f;
+    return;
+  }
   const char* x = reinterpret_cast<const char*>(a.X[g]) + r * a.ldx[g] * (a.bf16 ? 2 : 4);
   RowRaw<TPR, NV, MODE> raw;
   float v[NV][8];
@@ -346,7 +351,8 @@ __global__ void __launch_bounds__(256) col_amax_kernel(const __grid_constant__ Q
   float m[kE];
 #pragma unroll
   for (int i = 0; i < kE; ++i) m[i] = 0.f;
-  if (a.vecx && c + kE <= a.cols) {
+  const bool wide = a.vecx && (strip + 1) * 32 * kE <= a.cols;
+  if (wide) {
     const char* p = reinterpret_cast<const char*>(a.X) + c * (BF ? 2 : 4);
     const int64_t pitch = a.ldx * (BF ? 2 : 4);
     for (int64_t r = ra + warp; r < rb; r += 8 * kU) {
@@ -371,13 +377,36 @@ __global__ void __launch_bounds__(256) col_amax_kernel(const __grid_constant__ Q
       }
     }
   } else {
-    for (int64_t r = ra + warp; r < rb; r += 8)
+    // element by element: a lane's columns 32 apart, four rows in flight.  What
+    // is past the end reads the last one again: a maximum does not mind, and
+    // loads without conditions are issued together.
+    using E = std::conditional_t<BF, uint16_t, uint32_t>;
+    const int64_t ce = strip * 32 * kE + lane;
+    int at[kE];
 #pragma unroll
-      for (int i = 0; i < kE; ++i)
-        if (c + i < a.cols) m[i] = max_mag(m[i], ld1(a.X, r * a.ldx + c + i, BF));
+    for (int i = 0; i < kE; ++i)
+      at[i] = (int)(ce + 32 * i < a.cols ? ce + 32 * i : a.cols - 1);
+    for (int64_t r = ra + warp; r < rb; r += 8 * 4) {
+      uint32_t v[4][kE];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const E* x = reinterpret_cast<const E*>(a.X) + (r + 8 * k < rb ? r + 8 * k : rb - 1) * a.ldx;
+#pragma unroll
+        for (int i = 0; i < kE; ++i) v[k][i] = x[at[i]];
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int i = 0; i < kE; ++i)
+          m[i] = max_mag(m[i], __uint_as_float(BF ? v[k][i] << 16 : v[k][i]));
+    }
   }
+  // red[warp][column of the strip / kE][% kE], whichever way they were read
 #pragma unroll
-  for (int i = 0; i < kE; ++i) red[warp][lane][i] = m[i];
+  for (int i = 0; i < kE; ++i) {
+    const int e = wide ? lane * kE + i : 32 * i + lane;
+    red[warp][e / kE][e % kE] = m[i];
+  }
   __syncthreads();
   for (int e = threadIdx.x; e < 32 * kE; e += 256) {
     float v = 0.f;
@@ -397,7 +426,7 @@ constexpr int kOutPitch = kTileRows + 16;
 template <int BF>
 __global__ void __launch_bounds__(256, 4)
 quant_tile_kernel(const __grid_constant__ QuantT2Args a) {
-  constexpr int kCols = BF ? 64 : 32, kE = BF ? 8 : 4;
+  constexpr int kCols = BF ? 64 : 32;
   extern __shared__ __align__(16) uint32_t dyn[];
   uint32_t(*tile)[32] = reinterpret_cast<uint32_t(*)[32]>(dyn);
   // the tile's transpose: row e * 32 + l for column 2 l + e (fp32: l), pitch
@@ -418,17 +447,26 @@ quant_tile_kernel(const __grid_constant__ QuantT2Args a) {
       if (l < nr) ptx::copy16(&tile[l][piece * 4], p + l * pitch);
     }
   } else {
-    for (int l = threadIdx.x >> 3; l < nr; l += 32) {
-      uint32_t w[4] = {0, 0, 0, 0};
+    // element by element, a warp per row, eight rows in flight; what is past the
+    // end reads the last one again and is not used
+    using E = std::conditional_t<BF, uint16_t, uint32_t>;
+    int at[kCols / 32];
 #pragma unroll
-      for (int i = 0; i < kE; ++i) {
-        const int64_t c = c0 + piece * kE + i;
-        if (c >= a.cols) break;
-        const int64_t at = (r0 + l) * a.ldx + c;
-        if (BF) w[i >> 1] |= (uint32_t)reinterpret_cast<const uint16_t*>(a.X)[at] << (16 * (i & 1));
-        else w[i & 3] = reinterpret_cast<const uint32_t*>(a.X)[at];
+    for (int i = 0; i < kCols / 32; ++i)
+      at[i] = (int)(c0 + lane + 32 * i < a.cols ? c0 + lane + 32 * i : a.cols - 1);
+    for (int l0 = warp; l0 < nr; l0 += 64) {
+      uint32_t v[8][kCols / 32];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const E* x = reinterpret_cast<const E*>(a.X) + (r0 + min(l0 + 8 * k, nr - 1)) * a.ldx;
+#pragma unroll
+        for (int i = 0; i < kCols / 32; ++i) v[k][i] = x[at[i]];
       }
-      *reinterpret_cast<uint4*>(&tile[l][piece * 4]) = make_uint4(w[0], w[1], w[2], w[3]);
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+#pragma unroll
+        for (int i = 0; i < kCols / 32; ++i)
+          if (l0 + 8 * k < nr) reinterpret_cast<E*>(tile[l0 + 8 * k])[lane + 32 * i] = (E)v[k][i];
     }
   }
   // the columns' magnitudes, a group of threads per range of splits
@@ -613,7 +651,9 @@ extern "C" int quantize_int8(const ouo_mat* X, int x_dtype, const ouo_mat* Q, fl
     int mode = bf16 ? 1 : 2;
     for (int i = 0; i < cn; ++i)
       if (!a.vecx[i] || a.cols[i] % 8 != 0) mode = bf16 ? 3 : 4;
-    const Team t = team_for(acc, longest);
+    // (element by element too, a quantized row is one load and one store: the
+    // smaller teams of the vector modes do better)
+    const Team t = team_for(acc, longest, bf16 ? 1 : 2);
     if (t.tpr == 0) {
       quant_long_kernel<<<(unsigned)acc, 512, 0, s>>>(a);
       OUO_CHECK_LAUNCH();
