@@ -15,7 +15,6 @@
 namespace ouo {
 namespace {
 
-constexpr int kDThreads = 256;
 constexpr float kLowest = -3.402823466e38f;  // finite: -inf - m stays -inf
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -44,6 +43,7 @@ struct Teacher {
   alignas(16) int idx[OUO_DISTILL_MAX_ENTRIES];
 };
 
+template <int TH>
 __device__ __forceinline__ float block_fmax(float v, float* red) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
@@ -51,10 +51,11 @@ __device__ __forceinline__ float block_fmax(float v, float* red) {
   __syncthreads();
   v = red[0];
 #pragma unroll
-  for (int i = 1; i < kDThreads / 32; ++i) v = fmaxf(v, red[i]);
+  for (int i = 1; i < TH / 32; ++i) v = fmaxf(v, red[i]);
   return v;
 }
 
+template <int TH>
 __device__ __forceinline__ float block_fsum(float v, float* red) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -62,18 +63,19 @@ __device__ __forceinline__ float block_fsum(float v, float* red) {
   __syncthreads();
   v = red[0];
 #pragma unroll
-  for (int i = 1; i < kDThreads / 32; ++i) v += red[i];
+  for (int i = 1; i < TH / 32; ++i) v += red[i];
   return v;
 }
 
 // The row's teacher entries in shared memory: idx = -1 for one that does not
 // count (index outside the vocabulary, logit -inf).  False if none counts.
 // red: two sets of words for the two reductions.
+template <int TH>
 __device__ __forceinline__ bool teacher_probs(const DistillArgs& a, int64_t row, Teacher& t,
-                                              float (*red)[kDThreads / 32]) {
+                                              float (*red)[TH / 32]) {
   float m = kLowest;
   int some = 0;
-  for (int k = threadIdx.x; k < a.K; k += kDThreads) {
+  for (int k = threadIdx.x; k < a.K; k += TH) {
     int i = a.I[row * a.ldi + k];
     const float v = ld1(a.T, row * a.ldt + k, a.t_bf16) * a.inv_tau;
     if (i < 0 || i >= a.V || v == -INFINITY) i = -1;
@@ -89,16 +91,16 @@ __device__ __forceinline__ bool teacher_probs(const DistillArgs& a, int64_t row,
     if (k < OUO_DISTILL_MAX_ENTRIES) t.idx[k] = -1;
   }
   if (__syncthreads_or(some) == 0) return false;
-  m = block_fmax(m, red[0]);
+  m = block_fmax<TH>(m, red[0]);
   float z = 0.f;
-  for (int k = threadIdx.x; k < a.K; k += kDThreads) {
+  for (int k = threadIdx.x; k < a.K; k += TH) {
     t.lp[k] -= m;
     t.p[k] = t.idx[k] >= 0 ? expf(t.lp[k]) : 0.f;
     z += t.p[k];
   }
-  z = block_fsum(z, red[1]);
+  z = block_fsum<TH>(z, red[1]);
   const float lz = logf(z), iz = 1.f / z;
-  for (int k = threadIdx.x; k < a.K; k += kDThreads) {  // the thread's own entries
+  for (int k = threadIdx.x; k < a.K; k += TH) {  // the thread's own entries
     t.lp[k] -= lz;
     t.p[k] *= iz;
   }
@@ -150,13 +152,13 @@ struct Soft {
 // Bound by HBM: 4096 x 131072 bf16 in 171 us, 6.3 TB/s (191 without the prefetch).
 // One row per cluster: its CTAs divide the vocabulary and join their maxima
 // and sums through distributed shared memory (one CTA: no join).
-template <int BF>
-__global__ void __launch_bounds__(kDThreads, 4)
+template <int BF, int TH>
+__global__ void __launch_bounds__(TH, 1024 / TH)
 distill_kernel(const __grid_constant__ DistillArgs a) {
   constexpr int kU = BF ? 4 : 2;  // chunks of 8 in flight per thread
   __shared__ Teacher t;
-  __shared__ float red[4][kDThreads / 32];
-  __shared__ double redd[kDThreads / 32];
+  __shared__ float red[4][TH / 32];
+  __shared__ double redd[TH / 32];
   __shared__ float join[2];
   uint32_t nct;
   asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(nct));
@@ -173,19 +175,19 @@ distill_kernel(const __grid_constant__ DistillArgs a) {
   // kU chunks at a time, the next ones on their way while these are summed (the
   // first ones while the teacher's entries are)
   constexpr int kN = kU * (BF ? 1 : 2);
-  constexpr int64_t kStep = (int64_t)8 * kDThreads * kU;
+  constexpr int64_t kStep = (int64_t)8 * TH * kU;
   auto fetch = [&](uint4 (&raw)[kN], int64_t at) {
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
-      const uint4* p = reinterpret_cast<const uint4*>(s + (at + 8 * kDThreads * u) * (BF ? 2 : 4));
+      const uint4* p = reinterpret_cast<const uint4*>(s + (at + 8 * TH * u) * (BF ? 2 : 4));
 #pragma unroll
       for (int h = 0; h < kN / kU; ++h) raw[u * (kN / kU) + h] = __ldcs(p + h);
     }
   };
-  auto whole = [&](int64_t at) { return at + 8 * kDThreads * (kU - 1) < r.jb; };
+  auto whole = [&](int64_t at) { return at + 8 * TH * (kU - 1) < r.jb; };
   uint4 cur[kN];
   if (whole(j)) fetch(cur, j);
-  const bool any = teacher_probs(a, row, t, red);  // the same in every CTA of the cluster
+  const bool any = teacher_probs<TH>(a, row, t, red);  // the same in every CTA of the cluster
   if (!any) {
     if (threadIdx.x == 0 && rank == 0) {
       a.loss[row] = 0.f;
@@ -218,15 +220,15 @@ distill_kernel(const __grid_constant__ DistillArgs a) {
     for (int i = 0; i < kN; ++i) cur[i] = next[i];
     j += kStep;
   }
-  for (; j < r.jb; j += 8 * kDThreads) {
+  for (; j < r.jb; j += 8 * TH) {
     float v[8];
     ld8(s, j, BF, v);
     f.add(v, c);
   }
   if (r.jb + threadIdx.x < j1) f.add1(ld1(s, r.jb + threadIdx.x, BF), c);
 
-  float M = block_fmax(f.m, red[2]);
-  float Z = block_fsum(f.z * ex2((f.m - M) * c), red[3]);
+  float M = block_fmax<TH>(f.m, red[2]);
+  float Z = block_fsum<TH>(f.z * ex2((f.m - M) * c), red[3]);
   if (nct > 1) {
     if (threadIdx.x == 0) {
       join[0] = M;
@@ -257,7 +259,7 @@ distill_kernel(const __grid_constant__ DistillArgs a) {
   // student is near the teacher.
   const double lse = (double)M * (double)a.inv_tau + log((double)Z);
   double acc = 0.0;
-  for (int k = threadIdx.x; k < a.K; k += kDThreads) {
+  for (int k = threadIdx.x; k < a.K; k += TH) {
     const int i = t.idx[k];
     const float p = t.p[k];
     if (i < 0 || p == 0.f) continue;  // p = 0 also where the student's logit is -inf
@@ -269,7 +271,7 @@ distill_kernel(const __grid_constant__ DistillArgs a) {
   if ((threadIdx.x & 31) == 0) redd[threadIdx.x >> 5] = acc;
   __syncthreads();
   if (threadIdx.x == 0) {
-    for (int w = 1; w < kDThreads / 32; ++w) acc += redd[w];
+    for (int w = 1; w < TH / 32; ++w) acc += redd[w];
     a.loss[row] = (float)((double)a.tau * (double)a.tau * acc);
     a.lse[row] = (float)lse;
   }
@@ -277,38 +279,38 @@ distill_kernel(const __grid_constant__ DistillArgs a) {
 
 // Every CTA writes one segment of one row.  Bound by HBM: 4096 x 131072 bf16 in
 // 359 us, 6.0 TB/s.
-template <int BF>
-__global__ void __launch_bounds__(kDThreads, 4)
+template <int BF, int TH>
+__global__ void __launch_bounds__(TH, 1024 / TH)
 distill_bwd_kernel(const __grid_constant__ DistillArgs a, int64_t seg, int segs) {
   constexpr int kU = BF ? 4 : 2;
   __shared__ Teacher t;
   __shared__ float sq[OUO_DISTILL_MAX_ENTRIES];
-  __shared__ float red[2][kDThreads / 32];
+  __shared__ float red[2][TH / 32];
   const int64_t row = blockIdx.x / segs;
   const int64_t j0 = (blockIdx.x - row * segs) * seg;
   const int64_t j1 = j0 + seg < a.V ? j0 + seg : a.V;
   const float g = a.dloss[row] * a.tau, lse = a.lse[row];
   const char* s = reinterpret_cast<const char*>(a.S) + row * a.lds * (BF ? 2 : 4);
   char* d = reinterpret_cast<char*>(a.dS) + row * a.ldds * (a.ds_bf16 ? 2 : 4);
-  const bool any = g != 0.f && teacher_probs(a, row, t, red);
+  const bool any = g != 0.f && teacher_probs<TH>(a, row, t, red);
   // chunks that are 16-byte pieces of both matrices
   Run r = split_run(s, BF ? 2 : 4, j0, j1);
   if (((uintptr_t)d + r.ja * (a.ds_bf16 ? 2 : 4)) & 15) r.ja = r.jb = j0;
   auto prob = [&](float x) { return ex2((x * a.inv_tau - lse) * kLog2e); };
   if (any) {
     // dS may be S itself: the entries' own probabilities are read first
-    for (int k = threadIdx.x; k < a.K; k += kDThreads) {
+    for (int k = threadIdx.x; k < a.K; k += TH) {
       const int i = t.idx[k];
       if (i >= j0 && i < j1) sq[k] = prob(ld1(s, i, BF));
     }
     __syncthreads();
     auto one = [&](int64_t j) { st1(d, j, g * prob(ld1(s, j, BF)), a.ds_bf16); };
-    for (int64_t j = j0 + threadIdx.x; j < r.ja; j += kDThreads) one(j);
-    for (int64_t j = r.ja + 8 * threadIdx.x; j < r.jb; j += 8 * kDThreads * kU) {
+    for (int64_t j = j0 + threadIdx.x; j < r.ja; j += TH) one(j);
+    for (int64_t j = r.ja + 8 * threadIdx.x; j < r.jb; j += 8 * TH * kU) {
       uint4 raw[kU * (BF ? 1 : 2)];
 #pragma unroll
       for (int u = 0; u < kU; ++u) {
-        const int64_t e = j + 8 * kDThreads * u;
+        const int64_t e = j + 8 * TH * u;
         if (e >= r.jb) break;
         const uint4* p = reinterpret_cast<const uint4*>(s + e * (BF ? 2 : 4));
         if (BF) {
@@ -320,7 +322,7 @@ distill_bwd_kernel(const __grid_constant__ DistillArgs a, int64_t seg, int segs)
       }
 #pragma unroll
       for (int u = 0; u < kU; ++u) {
-        const int64_t e = j + 8 * kDThreads * u;
+        const int64_t e = j + 8 * TH * u;
         if (e >= r.jb) break;
         float v[8];
         if (BF) {
@@ -337,11 +339,11 @@ distill_bwd_kernel(const __grid_constant__ DistillArgs a, int64_t seg, int segs)
         st8(d, e, a.ds_bf16, v);
       }
     }
-    for (int64_t j = r.jb + threadIdx.x; j < j1; j += kDThreads) one(j);
+    for (int64_t j = r.jb + threadIdx.x; j < j1; j += TH) one(j);
     __syncthreads();
     // the first entry of each index takes every entry of that index
     const int4* i4 = reinterpret_cast<const int4*>(t.idx);
-    for (int k = threadIdx.x; k < a.K; k += kDThreads) {
+    for (int k = threadIdx.x; k < a.K; k += TH) {
       const int i = t.idx[k];
       if (i < j0 || i >= j1) continue;
       float p = 0.f;
@@ -362,10 +364,19 @@ distill_bwd_kernel(const __grid_constant__ DistillArgs a, int64_t seg, int segs)
     }
   } else {
     const float zero[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    for (int64_t j = j0 + threadIdx.x; j < r.ja; j += kDThreads) st1(d, j, 0.f, a.ds_bf16);
-    for (int64_t j = r.ja + 8 * threadIdx.x; j < r.jb; j += 8 * kDThreads) st8(d, j, a.ds_bf16, zero);
-    for (int64_t j = r.jb + threadIdx.x; j < j1; j += kDThreads) st1(d, j, 0.f, a.ds_bf16);
+    for (int64_t j = j0 + threadIdx.x; j < r.ja; j += TH) st1(d, j, 0.f, a.ds_bf16);
+    for (int64_t j = r.ja + 8 * threadIdx.x; j < r.jb; j += 8 * TH) st8(d, j, a.ds_bf16, zero);
+    for (int64_t j = r.jb + threadIdx.x; j < j1; j += TH) st1(d, j, 0.f, a.ds_bf16);
   }
+}
+
+// 128 threads a CTA rather than 256: for short runs of logits, where a row's
+// barriers count (4096 x 8192 bf16: loss 31.7 -> 22.3 us, gradient 43.8 -> 32.1),
+// and where the larger CTAs would fill the GPU between once and one and a half
+// times (700 x 131072: 39.9 -> 36.6, 80.3 -> 68.7).  Else 256 keep more of a row
+// on its way (gradient of 4096 x 131072: 359 us against 380).
+bool small_blocks(int64_t logits, int64_t ctas) {
+  return logits <= 16384 || (ctas > 4 * num_sms() && ctas < 6 * num_sms());
 }
 
 int check_distill(const ouo_mat* S, int s_dtype, const ouo_mat* teacher, int t_dtype,
@@ -420,15 +431,16 @@ int distill_loss(const ouo_mat* S, int s_dtype, const ouo_mat* teacher, int t_dt
   DistillArgs a = distill_args(S, s_dtype, teacher, t_dtype, idx, temperature);
   a.loss = loss;
   a.lse = lse;
-  // Few rows: a cluster per row, so that a GPU's worth of CTAs read it; a CTA
-  // keeps at least 4096 logits.
+  // Few rows: a cluster per row, as long as all CTAs are resident together; a
+  // CTA keeps at least 4096 logits.
   unsigned cluster = 1;
-  while (cluster < 8 && a.rows * cluster < 4 * num_sms() && a.V / (2 * cluster) >= 4096) cluster *= 2;
+  while (cluster < 8 && a.rows * 2 * cluster <= 4 * num_sms() && a.V / (2 * cluster) >= 4096) cluster *= 2;
   if (a.rows * cluster > 0x7fffffff) return set_error(OUO_ERR_UNSUPPORTED, "S: too many rows");
+  const bool small = small_blocks(ceil_div(a.V, (int64_t)cluster), a.rows * cluster);
   cudaLaunchConfig_t cfg;
   memset(&cfg, 0, sizeof(cfg));
   cfg.gridDim = dim3((unsigned)(a.rows * cluster), 1, 1);
-  cfg.blockDim = dim3(kDThreads, 1, 1);
+  cfg.blockDim = dim3(small ? 128 : 256, 1, 1);
   cfg.stream = (cudaStream_t)stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -437,7 +449,9 @@ int distill_loss(const ouo_mat* S, int s_dtype, const ouo_mat* teacher, int t_dt
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  OUO_CHECK_CUDA(cudaLaunchKernelEx(&cfg, a.s_bf16 ? distill_kernel<1> : distill_kernel<0>, a));
+  auto kern = a.s_bf16 ? (small ? distill_kernel<1, 128> : distill_kernel<1, 256>)
+                       : (small ? distill_kernel<0, 128> : distill_kernel<0, 256>);
+  OUO_CHECK_CUDA(cudaLaunchKernelEx(&cfg, kern, a));
   OUO_CHECK_LAUNCH();
   return OUO_OK;
 }
@@ -461,8 +475,9 @@ int distill_loss_backward(const ouo_mat* S, int s_dtype, const ouo_mat* teacher,
   a.lse = const_cast<float*>(lse);
   a.dloss = dloss;
   a.dS = dS->ptr; a.ldds = dS->ld; a.ds_bf16 = ds_dtype == OUO_BF16;
-  // Few rows are cut into segments, of 2048 logits at least.
-  int64_t segs = ceil_div((int64_t)8 * num_sms(), a.rows);
+  // Few rows are cut into segments, as many as are resident together, of 2048
+  // logits at least.
+  int64_t segs = (int64_t)4 * num_sms() / a.rows;
   if (segs > a.V / 2048) segs = a.V / 2048;
   if (segs < 1) segs = 1;
   const int64_t seg = ceil_div(ceil_div(a.V, segs), (int64_t)8) * 8;
@@ -470,8 +485,10 @@ int distill_loss_backward(const ouo_mat* S, int s_dtype, const ouo_mat* teacher,
   if (a.rows * segs > 0x7fffffff) return set_error(OUO_ERR_UNSUPPORTED, "S: too many rows");
   const unsigned grid = (unsigned)(a.rows * segs);
   cudaStream_t s = (cudaStream_t)stream;
-  if (a.s_bf16) distill_bwd_kernel<1><<<grid, kDThreads, 0, s>>>(a, seg, (int)segs);
-  else distill_bwd_kernel<0><<<grid, kDThreads, 0, s>>>(a, seg, (int)segs);
+  const bool small = small_blocks(seg, a.rows * segs);
+  auto kern = a.s_bf16 ? (small ? distill_bwd_kernel<1, 128> : distill_bwd_kernel<1, 256>)
+                       : (small ? distill_bwd_kernel<0, 128> : distill_bwd_kernel<0, 256>);
+  kern<<<grid, small ? 128 : 256, 0, s>>>(a, seg, (int)segs);
   OUO_CHECK_LAUNCH();
   return OUO_OK;
 }

@@ -31,7 +31,7 @@ __device__ __forceinline__ const char* row_of(const void* p, int64_t r, int64_t 
 
 // A team per row, h in registers (as the values that H's type holds): x and
 // the residual are read once, and nothing is read back.  Bound by HBM: 16384 x
-// 4096 bf16 with residual and 8-bit output in 72 us, 6.5 TB/s; with types asked
+// 4096 bf16 with residual and 8-bit output in 71 us, 6.6 TB/s; with types asked
 // for at run time it was 92 us, bound by instructions.
 template <int TPR, int NV, int MODE>
 __global__ void __launch_bounds__(kTeamThreads<TPR>) rms_kernel(const __grid_constant__ NormArgs a) {
@@ -179,8 +179,8 @@ struct NormBwdArgs {
 // and leaves once, to row b of the partial sums.  In modes 1 and 2 DEPTH rows of dY, H and dH are on their way
 // to shared memory (cp.async, to slots that only the copying warp reads, so
 // without block barriers), since the reduction of a row would otherwise leave the
-// memory idle (16384 x 4096 bf16: 180 us without, 88 us with it and with 16
-// elements a thread; HBM-bound at 6.1 TB/s).
+// memory idle (16384 x 4096 bf16: 180 us without, 87 us with it and with 16
+// elements a thread; HBM-bound at 6.2 TB/s).
 template <int TPR, int NV, int MODE, int DEPTH>
 __global__ void __launch_bounds__(TPR) rms_bwd_kernel(const __grid_constant__ NormBwdArgs a) {
   __shared__ float red[2][TPR / 32];
