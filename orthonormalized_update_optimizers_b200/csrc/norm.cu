@@ -171,7 +171,7 @@ struct NormBwdArgs {
   void* dX; int64_t lddx; int dx_bf16;
   float* part;
   int64_t rows, cols;
-  int vdy, vh, vw, vdh, vdx;  // 16-byte accesses allowed
+  int vdy, vh, vw, vdh, vdx, vpart;  // 16-byte accesses allowed
 };
 
 // A block of TPR threads takes rows b, b + grid, ...; every thread keeps the
@@ -309,7 +309,7 @@ __global__ void __launch_bounds__(TPR) rms_bwd_kernel(const __grid_constant__ No
     } else {
 #pragma unroll
       for (int c = 0; c < NV; ++c)
-        row_st8(part, 8 * (t + c * TPR), n, 0, n % 4 == 0, dw[c]);
+        row_st8(part, 8 * (t + c * TPR), n, 0, a.vpart, dw[c]);
     }
   }
 }
@@ -387,9 +387,11 @@ int launch_bwd(const NormBwdArgs& a, unsigned grid, cudaStream_t s) {
 }
 
 // Blocks of the gradient, and rows of partial sums of dw: what 148 SMs hold
-// at once.  A function of the shape alone, so that the workspace query needs
-// no device.
+// at once; one for a few tokens, whose sums are dw then, without a second
+// launch.  A function of the shape alone, so that the workspace query needs no
+// device.
 int64_t bwd_parts(int64_t rows, int64_t cols) {
+  if (rows > 0 && rows <= 8 && rows * cols <= 16384) return 1;
   const int64_t most = 148 * (cols <= 128 * 8 ? 7 : cols <= 128 * 16 ? 4 : cols <= 256 * 16 ? 2 : 1);
   return rows < most ? rows : most;
 }
@@ -477,7 +479,8 @@ int rms_norm(const ouo_mat* X, int x_dtype, const ouo_mat* residual, const ouo_m
 
 size_t rms_norm_backward_workspace_bytes(int64_t rows, int64_t cols) {
   if (rows < 0 || cols < 0) return 0;
-  return (size_t)(ouo::bwd_parts(rows, cols) * cols) * sizeof(float);
+  const int64_t parts = ouo::bwd_parts(rows, cols);
+  return parts > 1 ? (size_t)(parts * cols) * sizeof(float) : 0;
 }
 
 int rms_norm_backward(const ouo_mat* dY, int dy_dtype, const ouo_mat* H, int h_dtype,
@@ -522,7 +525,8 @@ int rms_norm_backward(const ouo_mat* dY, int dy_dtype, const ouo_mat* H, int h_d
     a.rstd = rstd;
     if (dH) { a.dH = dH->ptr; a.lddh = dH->ld; }
     a.dX = dX->ptr; a.lddx = dX->ld; a.dx_bf16 = dx_dtype == OUO_BF16;
-    a.part = dweight ? (float*)ws : nullptr;
+    a.part = !dweight ? nullptr : parts == 1 ? dweight : (float*)ws;
+    a.vpart = (uintptr_t)a.part % 16 == 0 && n % 4 == 0;
     a.rows = T; a.cols = n;
     a.vdy = rows16(*dY, elem_size(dy_dtype));
     a.vh = rows16(*H, elem_size(h_dtype));
@@ -541,7 +545,7 @@ int rms_norm_backward(const ouo_mat* dY, int dy_dtype, const ouo_mat* H, int h_d
       OUO_CHECK_LAUNCH();
     }
   }
-  if (dweight && n > 0) {
+  if (dweight && n > 0 && parts != 1) {
     rms_dw_kernel<<<(unsigned)ceil_div(n, 32), 512, 0, s>>>((const float*)ws, (int)parts, n,
                                                              dweight);
     OUO_CHECK_LAUNCH();
