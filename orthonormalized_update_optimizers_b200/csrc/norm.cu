@@ -175,12 +175,12 @@ struct NormBwdArgs {
 };
 
 // A block of TPR threads takes rows b, b + grid, ...; every thread keeps the
-// same columns of all of them, so that its share of dw stays in registers
-// and leaves once, to row b of the partial sums.  In modes 1 and 2 DEPTH rows of dY, H and dH are on their way
-// to shared memory (cp.async, to slots that only the copying warp reads, so
-// without block barriers), since the reduction of a row would otherwise leave the
-// memory idle (16384 x 4096 bf16: 180 us without, 87 us with it and with 16
-// elements a thread; HBM-bound at 6.2 TB/s).
+// same columns of all of them, so that its share of dw stays in registers and
+// leaves once, to row b of the partial sums.  In modes 1 and 2 DEPTH rows of dY,
+// H and dH are on their way to shared memory (cp.async, to slots that only the
+// copying warp reads, so without block barriers), since the reduction of a row
+// would otherwise leave the memory idle (16384 x 4096 bf16: 180 us without, 87 us
+// with it and with 16 elements a thread; HBM-bound at 6.2 TB/s).
 template <int TPR, int NV, int MODE, int DEPTH>
 __global__ void __launch_bounds__(TPR) rms_bwd_kernel(const __grid_constant__ NormBwdArgs a) {
   __shared__ float red[2][TPR / 32];

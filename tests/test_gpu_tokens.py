@@ -140,6 +140,21 @@ def test_quantize_empty():
     assert (s == 0).all()
 
 
+@pytest.mark.parametrize("transpose", [False, True])
+def test_quantize_batch_with_empty_matrices(transpose):
+    shapes = [(0, 8), (5, 16), (3, 0), (0, 0), (7, 9), (0, 4)]
+    xs = [torch.randn(s, generator=_rng(i), device=DEV) for i, s in enumerate(shapes)]
+    qs = [ouo.int8_empty(n, m) if transpose else ouo.int8_empty(m, n) for m, n in shapes]
+    ss = [torch.full((q.shape[0] + 1,), 77.0, device=DEV) for q in qs]
+    ouo.quantize_int8(xs, qs, ss, transpose=transpose)
+    for x, q, s in zip(xs, qs, ss):
+        assert s[-1] == 77
+        if x.numel():
+            _check_quant(to64(q), to64(s[:-1]), to64(x).T if transpose else to64(x))
+        else:
+            assert (s[:-1] == 0).all()
+
+
 def test_quantize_many_matrices():
     """More matrices than one launch's table holds."""
     xs = [torch.randn((1 + i % 5, 1 + i % 37), generator=_rng(i), device=DEV) for i in range(300)]
