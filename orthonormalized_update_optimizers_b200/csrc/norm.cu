@@ -41,10 +41,11 @@ __global__ void __launch_bounds__(kTeamThreads<TPR>) rms_kernel(const __grid_con
   const int64_t row = (int64_t)blockIdx.x * kTeams + (kTeams > 1 ? threadIdx.x / TPR : 0);
   if (kTeams > 1 && row >= a.rows) return;
   const int t = threadIdx.x % TPR, n = (int)a.cols;
-  constexpr int kBf = MODE == 1 || MODE == 3;
-  const int xb = MODE ? kBf : a.x_bf16, hb = MODE ? kBf : a.h_bf16;
-  const int wb = MODE ? kBf : a.w_bf16, yb = MODE ? kBf : a.y_bf16;
-  RowRaw<TPR, NV, MODE> xr, rr;
+  constexpr int XM = MODE == 5 ? 1 : MODE, HM = MODE == 5 ? 2 : MODE;  // x and y, residual and h
+  const int xb = MODE ? XM == 1 || XM == 3 : a.x_bf16, yb = MODE ? xb : a.y_bf16;
+  const int hb = MODE ? HM == 1 || HM == 3 : a.h_bf16;
+  RowRaw<TPR, NV, XM> xr;
+  RowRaw<TPR, NV, HM> rr;
   float v[NV][8];
   xr.load(row_of(a.X, row, a.ldx, xb), t, n, xb, a.vx);
   if (a.R) {
@@ -61,7 +62,7 @@ __global__ void __launch_bounds__(kTeamThreads<TPR>) rms_kernel(const __grid_con
   }
   if (a.H) {
     char* h = const_cast<char*>(row_of(a.H, row, a.ldh, hb));
-    if (MODE == 1) {
+    if (HM == 1) {
 #pragma unroll
       for (int c = 0; c < NV; ++c) {
         const uint4 u = pack8(v[c]);
@@ -69,8 +70,8 @@ __global__ void __launch_bounds__(kTeamThreads<TPR>) rms_kernel(const __grid_con
         unpack8(u, v[c]);
       }
     } else {
-      store_row<TPR, NV, MODE>(h, t, n, hb, a.vh, v);
-      if (MODE == 0 || MODE == 3) {
+      store_row<TPR, NV, HM>(h, t, n, hb, a.vh, v);
+      if (HM == 0 || HM == 3) {
 #pragma unroll
         for (int c = 0; c < NV; ++c)
 #pragma unroll
@@ -83,15 +84,22 @@ __global__ void __launch_bounds__(kTeamThreads<TPR>) rms_kernel(const __grid_con
   for (int c = 0; c < NV; ++c)
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc = fmaf(v[c][i], v[c][i], acc);
-  // the weight is on its way while the squares are summed
-  RowRaw<TPR, NV, MODE> wr;
-  wr.load(a.W, t, n, wb, a.vw);
+  // a weight of x's type is on its way while the squares are summed
+  RowRaw<TPR, NV, XM> wr;
+  const bool same = MODE == 0 || a.w_bf16 == xb;
+  if (same) wr.load(a.W, t, n, a.w_bf16, a.vw);
   const float rstd = __frsqrt_rn(team_sum<TPR>(acc, reds) / (float)n + a.eps);
   if (a.rstd && t == 0) a.rstd[row] = rstd;
   float m = 0.f;
   {
     float w[NV][8];
-    wr.get(w);
+    if (same) {
+      wr.get(w);
+    } else {
+      RowRaw<TPR, NV, kOtherType<XM>> other;
+      other.load(a.W, t, n, a.w_bf16, a.vw);
+      other.get(w);
+    }
 #pragma unroll
     for (int c = 0; c < NV; ++c)
 #pragma unroll
@@ -101,11 +109,11 @@ __global__ void __launch_bounds__(kTeamThreads<TPR>) rms_kernel(const __grid_con
       }
   }
   if (a.Y)
-    store_row<TPR, NV, MODE>(const_cast<char*>(row_of(a.Y, row, a.ldy, yb)), t, n, yb, a.vy, v);
+    store_row<TPR, NV, XM>(const_cast<char*>(row_of(a.Y, row, a.ldy, yb)), t, n, yb, a.vy, v);
   if (!a.Q) return;
   const Quant q = quant_of(team_max<TPR>(__float_as_uint(m), redm));
   if (t == 0) a.scale[row] = q.scale;
-  store_q<TPR, NV, MODE>(a.Q + row * a.ldq, t, n, a.vq, v, q);
+  store_q<TPR, NV, XM>(a.Q + row * a.ldq, t, n, a.vq, v, q);
 }
 
 // Rows too long for registers: one block per row; h is read back (from H, or
@@ -174,9 +182,19 @@ struct NormBwdArgs {
   int vdy, vh, vw, vdh, vdx, vpart;  // 16-byte accesses allowed
 };
 
+// The mode of each matrix (see RowRaw), and the 16-byte pieces of its chunks.
+template <int MODE>
+struct BwdModes {
+  static constexpr int kDy = MODE == 5 ? 1 : MODE, kH = MODE == 5 ? 2 : MODE,
+                       kDx = MODE == 5 ? 2 : MODE;
+  static constexpr bool kRing = MODE == 1 || MODE == 2 || MODE == 5;
+  static constexpr int kU0 = kDy == 2 ? 2 : 1, kU1 = kH == 2 ? 2 : 1, kU2 = kDx == 2 ? 2 : 1;
+  static constexpr int kUnits = kU0 + kU1 + kU2;
+};
+
 // A block of TPR threads takes rows b, b + grid, ...; every thread keeps the
 // same columns of all of them, so that its share of dw stays in registers and
-// leaves once, to row b of the partial sums.  In modes 1 and 2 DEPTH rows of dY,
+// leaves once, to row b of the partial sums.  In modes 1, 2 and 5 DEPTH rows of dY,
 // H and dH are on their way to shared memory (cp.async, to slots that only the
 // copying warp reads, so without block barriers), since the reduction of a row
 // would otherwise leave the memory idle (16384 x 4096 bf16: 180 us without, 87 us
@@ -184,18 +202,23 @@ struct NormBwdArgs {
 template <int TPR, int NV, int MODE, int DEPTH>
 __global__ void __launch_bounds__(TPR) rms_bwd_kernel(const __grid_constant__ NormBwdArgs a) {
   __shared__ float red[2][TPR / 32];
-  extern __shared__ __align__(16) uint4 ring[];  // [DEPTH][3][NV][TPR][kUnits]
-  constexpr int kUnits = MODE == 2 ? 2 : 1;      // 16-byte pieces of a chunk
+  using M = BwdModes<MODE>;
+  extern __shared__ __align__(16) uint4 ring[];  // [DEPTH][NV][dY, H, dH][TPR pieces a unit]
   const int t = threadIdx.x, n = (int)a.cols;
-  constexpr bool kRing = MODE == 1 || MODE == 2;
-  constexpr int kBf = MODE == 1 || MODE == 3;
-  const int dyb = MODE ? kBf : a.dy_bf16, hb = MODE ? kBf : a.h_bf16;
-  const int dxb = MODE ? kBf : a.dx_bf16;
+  const int dyb = MODE ? M::kDy == 1 || M::kDy == 3 : a.dy_bf16;
+  const int hb = MODE ? M::kH == 1 || M::kH == 3 : a.h_bf16;
+  const int dxb = MODE ? M::kDx == 1 || M::kDx == 3 : a.dx_bf16;
   float w[NV][8], dw[NV][8];
-  if (MODE >= 3) {
-    RowRaw<TPR, NV, MODE> wr;
-    wr.load(a.W, t, n, kBf, 0);
-    wr.get(w);
+  if (MODE == 3 || MODE == 4) {
+    if (a.w_bf16) {
+      RowRaw<TPR, NV, 3> wr;
+      wr.load(a.W, t, n, 1, 0);
+      wr.get(w);
+    } else {
+      RowRaw<TPR, NV, 4> wr;
+      wr.load(a.W, t, n, 0, 0);
+      wr.get(w);
+    }
   } else {
 #pragma unroll
     for (int c = 0; c < NV; ++c) row_ld8(a.W, 8 * (t + c * TPR), n, a.w_bf16, a.vw, w[c]);
@@ -208,21 +231,26 @@ __global__ void __launch_bounds__(TPR) rms_bwd_kernel(const __grid_constant__ No
                         a.dH ? row_of(a.dH, blockIdx.x, a.lddh, dxb) : nullptr};
   const int64_t step[3] = {a.lddy * (dyb ? 2 : 4) * gridDim.x, a.ldh * (hb ? 2 : 4) * gridDim.x,
                            a.lddh * (dxb ? 2 : 4) * gridDim.x};
+  // slots of stage, chunk and matrix, in 16-byte pieces of the team
+  auto slot = [&](int stage, int c, int before) {
+    return ring + ((stage * NV + c) * M::kUnits + before) * TPR;
+  };
   auto issue = [&](int64_t row, int stage) {
     if (row < a.rows) {
 #pragma unroll
       for (int m = 0; m < 3; ++m) {
         if (m == 2 && !a.dH) break;
+        const int units = m == 0 ? M::kU0 : m == 1 ? M::kU1 : M::kU2;
+        const int before = m == 0 ? 0 : m == 1 ? M::kU0 : M::kU0 + M::kU1;
 #pragma unroll
         for (int c = 0; c < NV; ++c) {
 #pragma unroll
-          for (int u = 0; u < kUnits; ++u) {
+          for (int u = 0; u < units; ++u) {
             // a warp's copies of one instruction are 512 bytes in a row, so
             // with fp32 a lane's pieces are copied by other lanes of its warp
-            const int piece = (t & ~31) * kUnits + u * 32 + (t & 31);
-            if ((16 / kUnits) / 2 * (c * TPR * kUnits + piece) < n)
-              ptx::copy16(ring + ((stage * 3 + m) * NV + c) * kUnits * TPR + piece,
-                          src[m] + (c * TPR * kUnits + piece) * 16);
+            const int piece = (t & ~31) * units + u * 32 + (t & 31);
+            if ((units == 2 ? 4 : 8) * (c * TPR * units + piece) < n)
+              ptx::copy16(slot(stage, c, before) + piece, src[m] + (c * TPR * units + piece) * 16);
           }
         }
         src[m] += step[m];
@@ -230,17 +258,18 @@ __global__ void __launch_bounds__(TPR) rms_bwd_kernel(const __grid_constant__ No
     }
     ptx::copy16_commit();
   };
-  auto fetch = [&](auto& r, int stage, int m) {
+  auto fetch = [&](auto& r, int stage, int before, auto units) {
+    constexpr int kU = decltype(units)::value;
 #pragma unroll
     for (int c = 0; c < NV; ++c) {
       const bool in = 8 * (t + c * TPR) < n;
-      const uint4* q = ring + (((stage * 3 + m) * NV + c) * TPR + t) * kUnits;
+      const uint4* q = slot(stage, c, before) + t * kU;
       r.a[c] = in ? q[0] : make_uint4(0, 0, 0, 0);
-      if constexpr (MODE == 2) r.b[c] = in ? q[kUnits - 1] : make_uint4(0, 0, 0, 0);
+      if constexpr (kU == 2) r.b[c] = in ? q[1] : make_uint4(0, 0, 0, 0);
     }
   };
   int64_t ahead = blockIdx.x;
-  if constexpr (kRing) {
+  if constexpr (M::kRing) {
 #pragma unroll
     for (int s = 0; s < DEPTH; ++s, ahead += gridDim.x) issue(ahead, s);
   }
@@ -253,15 +282,16 @@ __global__ void __launch_bounds__(TPR) rms_bwd_kernel(const __grid_constant__ No
     const float r = r_next;
     if (row + gridDim.x < a.rows) r_next = a.rstd[row + gridDim.x];
     float g[NV][8], h[NV][8];
-    RowRaw<TPR, NV, MODE> dr;
+    RowRaw<TPR, NV, M::kDx> dr;
     {
-      RowRaw<TPR, NV, MODE> gr, hr;
-      if constexpr (kRing) {
+      RowRaw<TPR, NV, M::kDy> gr;
+      RowRaw<TPR, NV, M::kH> hr;
+      if constexpr (M::kRing) {
         asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 1) : "memory");
-        if (MODE == 2) __syncwarp();
-        fetch(gr, stage, 0);
-        fetch(hr, stage, 1);
-        if (a.dH) fetch(dr, stage, 2);
+        if (MODE != 1) __syncwarp();
+        fetch(gr, stage, 0, C<M::kU0>{});
+        fetch(hr, stage, M::kU0, C<M::kU1>{});
+        if (a.dH) fetch(dr, stage, M::kU0 + M::kU1, C<M::kU2>{});
       } else {
         gr.load(row_of(a.dY, row, a.lddy, dyb), t, n, dyb, a.vdy);
         hr.load(row_of(a.H, row, a.ldh, hb), t, n, hb, a.vh);
@@ -293,18 +323,18 @@ __global__ void __launch_bounds__(TPR) rms_bwd_kernel(const __grid_constant__ No
 #pragma unroll
         for (int i = 0; i < 8; ++i) g[c][i] += h[c][i];
     }
-    if constexpr (kRing) {  // this stage's values are in registers
-      if (MODE == 2) __syncwarp();
+    if constexpr (M::kRing) {  // this stage's values are in registers
+      if (MODE != 1) __syncwarp();
       issue(ahead, stage);
       ahead += gridDim.x;
       if (++stage == DEPTH) stage = 0;
     }
-    store_row<TPR, NV, MODE>(dx, t, n, dxb, a.vdx, g);
+    store_row<TPR, NV, M::kDx>(dx, t, n, dxb, a.vdx, g);
   }
-  if (kRing) ptx::copy16_wait_all();
+  if (M::kRing) ptx::copy16_wait_all();
   if (a.part) {
     float* part = a.part + blockIdx.x * a.cols;
-    if (MODE >= 3) {
+    if (MODE == 3 || MODE == 4) {
       store_row<TPR, NV, 4>(part, t, n, 0, 0, dw);
     } else {
 #pragma unroll
@@ -365,7 +395,8 @@ rms_dw_kernel(const float* part, int nparts, int64_t cols, float* dw) {
 
 template <int TPR, int NV, int MODE, int DEPTH>
 int launch_bwd_as(const NormBwdArgs& a, unsigned grid, cudaStream_t s) {
-  constexpr size_t kSmem = MODE == 1 || MODE == 2 ? (size_t)DEPTH * 3 * NV * TPR * 16 * (MODE == 2 ? 2 : 1) : 0;
+  using M = BwdModes<MODE>;
+  constexpr size_t kSmem = M::kRing ? (size_t)DEPTH * M::kUnits * NV * TPR * 16 : 0;
   if (kSmem > 40 * 1024) {  // with the static part, past the default limit
     static Once once;
     OUO_TRY(once.smem(rms_bwd_kernel<TPR, NV, MODE, DEPTH>, kSmem));
@@ -379,10 +410,11 @@ template <int TPR, int NV>
 int launch_bwd(const NormBwdArgs& a, unsigned grid, cudaStream_t s) {
   const bool vec = a.vdy && a.vh && a.vdx && (a.vdh || !a.dH) && a.cols % 8 == 0;
   const int bf = a.dy_bf16 + a.h_bf16 + a.dx_bf16;
+  if (vec && bf == 1 && a.dy_bf16) return launch_bwd_as<TPR, NV, 5, 2>(a, grid, s);
   if (vec && bf == 3) return launch_bwd_as<TPR, NV, 1, 4>(a, grid, s);
   if (vec && bf == 0) return launch_bwd_as<TPR, NV, 2, 2>(a, grid, s);
-  if (bf == 3 && a.w_bf16) return launch_bwd_as<TPR, NV, 3, 1>(a, grid, s);
-  if (bf == 0 && !a.w_bf16) return launch_bwd_as<TPR, NV, 4, 1>(a, grid, s);
+  if (bf == 3) return launch_bwd_as<TPR, NV, 3, 1>(a, grid, s);
+  if (bf == 0) return launch_bwd_as<TPR, NV, 4, 1>(a, grid, s);
   return launch_bwd_as<TPR, NV, 0, 1>(a, grid, s);
 }
 
@@ -457,10 +489,12 @@ int rms_norm(const ouo_mat* X, int x_dtype, const ouo_mat* residual, const ouo_m
   a.vq = Q ? (uintptr_t)a.Q % 8 == 0 && (T <= 1 || a.ldq % 8 == 0) : 0;
   cudaStream_t s = (cudaStream_t)stream;
   const bool vec = a.vx && a.vw && (!a.R || a.vr) && (!a.H || a.vh) && (!a.Y || a.vy) && n % 8 == 0;
-  auto all = [&](int dt) {
-    return x_dtype == dt && w_dtype == dt && (!H || h_dtype == dt) && (!Y || y_dtype == dt);
+  auto all = [&](int dt, int hdt) {
+    return x_dtype == dt && (!H || h_dtype == hdt) && (!Y || y_dtype == dt);
   };
-  const int mode = all(OUO_BF16) ? (vec ? 1 : 3) : all(OUO_F32) ? (vec ? 2 : 4) : 0;
+  const int mode = all(OUO_BF16, OUO_BF16) ? (vec ? 1 : 3)
+                   : all(OUO_F32, OUO_F32) ? (vec ? 2 : 4)
+                   : all(OUO_BF16, OUO_F32) && vec ? 5 : 0;
   const Team t = team_for(T, n, mode);
   if (t.tpr == 0) {
     rms_long_kernel<<<(unsigned)T, 512, 0, s>>>(a);

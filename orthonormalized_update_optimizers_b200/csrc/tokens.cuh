@@ -231,7 +231,8 @@ __device__ __forceinline__ void row_st8(void* p, int j, int n, int bf16, int vec
 //         thread t is elements 8 (t + c TPR) .. + 7;
 //   3, 4: all bf16 / fp32, any alignment and n: element i of chunk c is
 //         (8 c + i) TPR + t, so that a warp's accesses lie next to each other;
-//   0:    mixed types: as 1 and 2, element by element where need be.
+//   5:    a bf16 layer on an fp32 residual stream (norm only): 1 and 2;
+//   0:    other mixtures: as 1 and 2, element by element where need be.
 template <int TPR, int NV, int MODE>
 struct RowRaw {
   uint4 a[MODE <= 2 ? NV : 1], b[MODE == 0 || MODE == 2 ? NV : 1];  // b: second half of fp32
@@ -284,6 +285,10 @@ struct RowRaw {
   }
 };
 
+// The mode of the same accesses to the other type.
+template <int MODE>
+constexpr int kOtherType = MODE == 1 ? 2 : MODE == 2 ? 1 : MODE == 3 ? 4 : MODE == 4 ? 3 : 0;
+
 template <int TPR, int NV, int MODE>
 __device__ __forceinline__ void store_row(void* p, int t, int n, int bf16, int vec,
                                           const float v[NV][8]) {
@@ -318,7 +323,7 @@ inline Team team_for(int64_t rows, int64_t cols, int mode) {
   const int64_t chunks = ceil_div(cols, (int64_t)8);
   int tpr = chunks <= 32 * 8 ? 32 : chunks <= 128 * 8 ? 128 : 512;
   if (chunks > 512 * 4) return Team{0, 0};
-  if (rows < 4 * num_sms() || mode >= 3) tpr = chunks <= 128 ? (chunks <= 32 ? 32 : 128) : 512;
+  if (rows < 4 * num_sms() || mode == 3 || mode == 4) tpr = chunks <= 128 ? (chunks <= 32 ? 32 : 128) : 512;
   int nv = 1;
   while ((int64_t)tpr * nv < chunks) nv *= 2;
   return Team{tpr, nv};
@@ -353,6 +358,7 @@ int with_team(Team t, int mode, F&& f) {
       case 2: return f(tpr, nv, C<2>{});
       case 3: return f(tpr, nv, C<3>{});
       case 4: return f(tpr, nv, C<4>{});
+      case 5: return f(tpr, nv, C<5>{});
       default: return f(tpr, nv, C<0>{});
     }
   });

@@ -332,6 +332,38 @@ def test_rms_norm_mixed_types_and_in_place():
     assert torch.equal(h, x.float())
 
 
+@pytest.mark.parametrize("rows,cols", [(3, 16), (700, 1000), (1300, 2048), (333, 4096), (40, 8192),
+                                       (50, 1001), (3, 20008)])
+@pytest.mark.parametrize("types", [(BF, F32, BF), (BF, F32, F32), (BF, BF, F32), (F32, F32, BF),
+                                   (F32, BF, F32)])
+def test_rms_norm_types(rows, cols, types):
+    """x / y, residual / h / gradient stream and weight of different types,
+    forward and backward."""
+    dt, ht, wt = types
+    g = _rng(cols)
+    x = torch.randn((rows, cols), generator=g, device=DEV).to(dt)
+    r = torch.randn((rows, cols), generator=g, device=DEV).to(ht)
+    w = (torch.rand(cols, generator=g, device=DEV) + 0.5).to(wt)
+    h, y, q = torch.empty_like(r), torch.empty_like(x), ouo.int8_empty(rows, cols)
+    scale, rstd = torch.empty(rows, device=DEV), torch.empty(rows, device=DEV)
+    ouo.rms_norm(x, w, Y=y, Q=q, scale=scale, residual=r, H=h, rstd=rstd, eps=1e-5)
+    assert torch.equal(h, (x.float() + r.float()).to(ht))
+    ye, re = ot.rms_norm(to64(h), to64(w), 1e-5)
+    tol = _sum_tol(cols) / 2 + 7 * U32
+    assert np.all(np.abs(to64(rstd) - re) <= tol * re)
+    assert np.all(np.abs(to64(y) - ye) <= (tol + UOUT[dt]) * np.abs(ye))
+    assert np.all(np.abs(to64(q) - ot.quantize(ye)[0]) <= 0.5 + 127 * (2 * tol + 4 * U32))
+    dy = torch.randn((rows, cols), generator=g, device=DEV).to(dt)
+    dh = torch.randn((rows, cols), generator=g, device=DEV).to(ht)
+    dx, dw = torch.empty_like(dh), torch.empty(cols, device=DEV)
+    ouo.rms_norm_backward(dy, h, w, rstd, dx, dweight=dw, dH=dh)
+    G, H, W, R, D = to64(dy), to64(h), to64(w), to64(rstd)[:, None], to64(dh)
+    ex, ew = ot.rms_norm_grad(G, H, W, R[:, 0], D)
+    mag = R * (np.abs(G * W) + np.abs(H) * R * R * np.mean(np.abs(G * W * H), 1, keepdims=True)) + np.abs(D)
+    assert np.all(np.abs(to64(dx) - ex) <= (_sum_tol(cols) + 8 * U32) * mag + UOUT[ht] * np.abs(ex))
+    assert np.all(np.abs(to64(dw) - ew) <= (rows + 34) * U32 * np.sum(np.abs(G * H * R), axis=0))
+
+
 def test_rms_norm_zero_and_nonfinite_rows():
     x = torch.randn((5, 256), generator=_rng(1), device=DEV)
     x[1] = 0
