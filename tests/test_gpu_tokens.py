@@ -570,6 +570,52 @@ def test_distill_no_rows():
     ouo.distill_loss_backward(e, torch.empty((0, 3), device=DEV), i, z, z, e)
 
 
+# ------------------------------------------------------ past 2^31 elements
+
+
+def test_offsets_past_32_bits():
+    """Matrices of more than 2^31 elements (and bytes): the last rows are
+    those of the same rows alone."""
+    last, tail = 3, lambda t: t[-3:].clone()
+    rows, vocab = 16500, 131072
+    s = torch.empty((rows, vocab), dtype=BF, device=DEV)
+    s[-last:] = torch.randn((last, vocab), generator=_rng(0), device=DEV) * 2
+    s[:-last] = 1.0
+    t, idx = _teacher(rows, vocab, 4, 1)
+    loss, lse = torch.empty(rows, device=DEV), torch.empty(rows, device=DEV)
+    ouo.distill_loss(s, t, idx, loss, lse)
+    a, b = torch.empty(last, device=DEV), torch.empty(last, device=DEV)
+    keep = tail(s)
+    ouo.distill_loss(keep, tail(t), tail(idx), a, b)
+    # the sums' order may be another with so few rows
+    assert torch.allclose(lse[-last:], b, rtol=4 * U32, atol=0)
+    assert torch.allclose(loss[-last:], a, rtol=1e-5, atol=1e-5)
+    dl = torch.ones(rows, device=DEV)
+    ouo.distill_loss_backward(s, t, idx, lse, dl, s)
+    d = torch.empty_like(keep)
+    ouo.distill_loss_backward(keep, tail(t), tail(idx), lse[-last:].contiguous(), dl[:last], d)
+    assert torch.equal(s[-last:], d)
+    # s again: 131072 columns as rows of 8-bit integers, both ways
+    x = s.view(rows * 16, vocab // 16)
+    x[-last:] = torch.randn((last, vocab // 16), generator=_rng(2), device=DEV)
+    q, sc = ouo.int8_empty(*x.shape), torch.empty(x.shape[0], device=DEV)
+    ouo.quantize_int8(x, q, sc)
+    _check_quant(to64(q[-last:]), to64(sc[-last:]), to64(x[-last:]))
+    ouo.rms_norm(x, torch.ones(x.shape[1], device=DEV), Q=q, scale=sc, eps=0.0)
+    y = ot.rms_norm(to64(x[-last:]), np.ones(x.shape[1]), 0.0)[0]
+    assert np.all(np.abs(to64(q[-last:]) - ot.quantize(y)[0]) <= 0.5 + 127 * _sum_tol(8192) * 2)
+    qt, st = ouo.int8_empty(x.shape[1], x.shape[0]), torch.empty(x.shape[1], device=DEV)
+    ouo.quantize_int8(x, qt, st, transpose=True)
+    cols = x[:, -last:].t().contiguous()
+    _check_quant(to64(qt[-last:]), to64(st[-last:]), to64(cols))
+    del s, x, q, qt
+    a8, b8 = ouo.int8_empty(66000, 64).copy_(_ints((66000, 64), 3)), ouo.int8_empty(33000, 64).copy_(_ints((33000, 64), 4))
+    sa, sb = torch.rand(66000, device=DEV), torch.rand(33000, device=DEV)
+    D = torch.empty((66000, 33000), dtype=BF, device=DEV)
+    ouo.int8_matmul(a8, sa, b8, sb, D)
+    _check_mm(D[-last:], a8[-last:], sa[-last:], b8, sb)
+
+
 # ------------------------------------------------- streams, graphs, repeats
 
 
