@@ -438,8 +438,8 @@ int dion_shard_update(const ouo_mat* M, const ouo_mat* Q_state,
  *   transpose 1:  scale_j = max_i |x_ij| / 127,  q_ji = rint(x_ij / scale_j)
  *                 Q[i] is cols x rows (X's columns are Q's rows), scale[i]
  *                 one float per row of Q[i].
- * (q may differ from the exact quotient's rounding where that lies within
- * 1e-5 of a half.)  An all-zero row gets scale 0 and zeros; a row with a NaN or
+ * (q is the exact quotient's rounding for bf16 X; for fp32 X a quotient within
+ * 1e-5 of a half, but not on it, may go either way.)  An all-zero row gets scale 0 and zeros; a row with a NaN or
  * an infinity gets scale NaN and zeros, so that every product with it is
  * NaN.  scale: host array of nmat device pointers.  X: dtype x_dtype.
  * Large transposed matrices need a workspace (16-byte aligned; 0 bytes

@@ -111,7 +111,7 @@ __global__ void __launch_bounds__(kTeamThreads<TPR>) rms_kernel(const __grid_con
   if (a.Y)
     store_row<TPR, NV, XM>(const_cast<char*>(row_of(a.Y, row, a.ldy, yb)), t, n, yb, a.vy, v);
   if (!a.Q) return;
-  const Quant q = quant_of(team_max<TPR>(__float_as_uint(m), redm));
+  const Quant q = quant_of<0>(team_max<TPR>(__float_as_uint(m), redm));
   if (t == 0) a.scale[row] = q.scale;
   store_q<TPR, NV, XM>(a.Q + row * a.ldq, t, n, a.vq, v, q);
 }
@@ -161,7 +161,7 @@ __global__ void __launch_bounds__(512) rms_long_kernel(const __grid_constant__ N
       row_st8(const_cast<char*>(row_of(a.Y, row, a.ldy, a.y_bf16)), j, n, a.y_bf16, a.vy, v);
   }
   if (!a.Q) return;
-  const Quant q = quant_of(block_max(__float_as_uint(m), red));
+  const Quant q = quant_of<0>(block_max(__float_as_uint(m), red));
   if (threadIdx.x == 0) a.scale[row] = q.scale;
   for (int j = 8 * threadIdx.x; j < n; j += 8 * 512) {
     float v[8];

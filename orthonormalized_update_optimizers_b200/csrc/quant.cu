@@ -62,7 +62,7 @@ quant_rows_kernel(const __grid_constant__ QuantArgs a) {
   for (int c = 0; c < NV; ++c)
 #pragma unroll
     for (int i = 0; i < 8; ++i) m = max_mag(m, v[c][i]);
-  const Quant q = quant_of(team_max<TPR>(__float_as_uint(m), red));
+  const Quant q = quant_of<MODE == 1 || MODE == 3>(team_max<TPR>(__float_as_uint(m), red));
   if (t == 0) a.scale[g][r] = q.scale;
   int8_t* o = a.Q[g] + r * a.ldq[g];
   store_q<TPR, NV, MODE>(o, t, n, a.vecq[g], v, q);
@@ -85,7 +85,7 @@ __global__ void __launch_bounds__(512) quant_long_kernel(const __grid_constant__
 #pragma unroll
     for (int i = 0; i < 8; ++i) m = max_mag(m, v[i]);
   }
-  const Quant q = quant_of(block_max(__float_as_uint(m), red));
+  const Quant q = quant_of<0>(block_max(__float_as_uint(m), red));
   if (threadIdx.x == 0) a.scale[g][r] = q.scale;
   for (int64_t j = 8 * threadIdx.x; j < n; j += 8 * 512) {
     float v[8];
@@ -223,7 +223,7 @@ quant_cols_kernel(const __grid_constant__ QuantTArgs a) {
   }
   __syncwarp();
   ptx::cluster_sync();  // everyone has read everyone's (nothing is read from afar below)
-  const Quant q0 = quant_of(x0), q1 = quant_of(x1);
+  const Quant q0 = quant_of<BF>(x0), q1 = quant_of<BF>(x1);
   const int64_t col = c0 + (BF ? 2 * wd : wd);
   if (rank == 0 && warp == 0 && half == 0) {
     if (col < a.cols) a.scale[col] = q0.scale;
@@ -490,11 +490,11 @@ quant_tile_kernel(const __grid_constant__ QuantT2Args a) {
 #pragma unroll
     for (int g = 0; g < kG; ++g) m = max(m, cm[g][threadIdx.x]);
     cm[0][threadIdx.x] = m;
-    if (tr == 0 && c0 + threadIdx.x < a.cols) a.scale[c0 + threadIdx.x] = quant_of(m).scale;
+    if (tr == 0 && c0 + threadIdx.x < a.cols) a.scale[c0 + threadIdx.x] = quant_of<BF>(m).scale;
   }
   __syncthreads();
-  const Quant q0 = quant_of(cm[0][BF ? 2 * lane : lane]);
-  const Quant q1 = BF ? quant_of(cm[0][2 * lane + 1]) : q0;
+  const Quant q0 = quant_of<BF>(cm[0][BF ? 2 * lane : lane]);
+  const Quant q1 = BF ? quant_of<BF>(cm[0][2 * lane + 1]) : q0;
   for (int b = warp * 16; b < nr; b += 128) {
     uint32_t w[16];
 #pragma unroll

@@ -365,20 +365,32 @@ int with_team(Team t, int mode, F&& f) {
 }
 
 // 8-bit rounding of a row with the largest magnitude `amax`:
-//   scale = amax / 127,  q = rint(x * (127 / amax)).
-// The quotient 127 / amax is rounded once, so x * inv is within one rounding
-// of x / scale and q differs from the exact quotient's rounding only where that
-// lies within 1e-5 of a half.  Below 2^-96 the reciprocal could overflow:
-// there x and amax are multiplied by 2^96 (exact) first.  A zero row has scale
-// 0 and zeros; a row with a NaN or an infinity has scale NaN and zeros, so
-// that what is computed from it is NaN.
+//   scale = amax / 127,  q = rint(x * (127 / amax)),  ties to even.
+// An fp32 product with a rounded quotient can land on either side of a half
+// that the exact value hits, and bf16 rows hit one often: x = amax / 2 is 63.5.
+// With amax = a 2^i and x = m 2^j (a, m odd) the quotient is (127 m / a) 2^(j-i),
+// a half-integer only if
+//   * a divides m: then it is 63.5, the only odd multiple of 127 / 2 up to 127,
+//     and 127 / amax rounded up keeps the product at or above it: 64;
+//   * or a = 127 b: then amax / 127 is an fp32 number.  If 127 / amax is one
+//     too (b = 1, the only such bf16 rows), products are exact.  Else (fp32
+//     rows only, one in 127) the division's remainder corrects the product.
+// So bf16 rows get the exact quotient's rounding; an fp32 quotient within
+// 1e-5 of a half, but not on it, may go either way.  Below 2^-96 the quotient
+// could overflow: there x and amax are multiplied by 2^96 (exact) first.  A
+// zero row has scale 0 and zeros; a row with a NaN or an infinity has scale NaN
+// and zeros, so that what is computed from it is NaN.
 struct Quant {
   float scale, inv, pre;
+  float unit;  // amax pre / 127 where products need the correction, else 0
 };
 
+// BF: the row is bf16, which no correction is needed for (and compiled into).
+template <int BF>
 __device__ __forceinline__ Quant quant_of(uint32_t amax_bits) {
   Quant q;
   const float amax = __uint_as_float(amax_bits);
+  q.unit = 0.f;
   if (amax_bits >= 0x7f800000u) {
     q.scale = __uint_as_float(0x7fc00000u);
     q.inv = 0.f;
@@ -387,25 +399,42 @@ __device__ __forceinline__ Quant quant_of(uint32_t amax_bits) {
   }
   q.scale = __fdiv_rn(amax, 127.f);
   q.pre = amax < 0x1p-96f ? 0x1p96f : 1.f;
-  q.inv = amax > 0.f ? __fdiv_rn(127.f, amax * q.pre) : 0.f;
+  const float a = amax * q.pre;
+  if (a > 0.f) {
+    q.inv = __fdiv_rn(127.f, a);
+    const float over = fmaf(q.inv, a, -127.f);  // of the rounded quotient, exact
+    if (over < 0.f) q.inv = __uint_as_float(__float_as_uint(q.inv) + 1u);
+    if (!BF) {
+      const float unit = q.pre == 1.f ? q.scale : __fdiv_rn(a, 127.f);
+      if (over != 0.f && fmaf(unit, 127.f, -a) == 0.f) q.unit = unit;
+    }
+  } else {
+    q.inv = 0.f;
+  }
   return q;
 }
 
-// The integer nearest to x * inv is in the low byte of x * inv + 1.5 * 2^23,
-// an fp32 sum whose last place is 1 (one rounding, to nearest even; |x * inv|
-// is at most 127 up to rounding, so nothing needs clamping).
+// The integer nearest to a value is in the low byte of its sum with 1.5 * 2^23,
+// an fp32 sum whose last place is 1 (to nearest even; |x * inv| is at most 127
+// up to rounding, so nothing needs clamping).
 constexpr float kMagic = 12582912.f;
 
 __device__ __forceinline__ int quant1(float x, const Quant& q) {
   if (q.pre == 0.f) return 0;
-  return (int8_t)(__float_as_uint(fmaf(x * q.pre, q.inv, kMagic)) & 255u);
+  const float v = x * q.pre;
+  float s = fmaf(v, q.inv, kMagic);
+  if (q.unit != 0.f) {
+    const float p = v * q.inv;
+    s = fmaf(fmaf(-p, q.unit, v), q.inv, p) + kMagic;
+  }
+  return (int8_t)(__float_as_uint(s) & 255u);
 }
 
-// Eight of them as 8 bytes; the rare rows that are not finite or tiny take
-// the second branch together.
+// Eight of them as 8 bytes; the rare rows that are not finite, tiny or
+// corrected take the second branch together.
 __device__ __forceinline__ uint2 quant8(const float v[8], const Quant& q) {
   uint32_t b[8];
-  if (q.pre == 1.f) {
+  if (q.pre == 1.f && q.unit == 0.f) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) b[i] = __float_as_uint(fmaf(v[i], q.inv, kMagic));
   } else {
