@@ -267,13 +267,23 @@ def gram_ns_workspace_bytes(X, params=None) -> int:
     return int(L.lib().gram_ns_workspace_bytes(Xb.arr, Xb.n, ctypes.byref(p)))
 
 
-def _workspace(nbytes: int, device, given: Optional[torch.Tensor]):
+def alloc_on(stream, n: int, dtype: torch.dtype, device) -> torch.Tensor:
+    """A buffer that only work on `stream` (None: the current one) touches:
+    from that stream's pool, since a block of another stream's may still be
+    in use there when this one starts on it."""
+    if stream is None:
+        return torch.empty(n, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(n, dtype=dtype, device=device)
+
+
+def _workspace(nbytes: int, device, given: Optional[torch.Tensor], stream):
     if given is not None:
         # an empty batch names no device index ("cuda"): check the rest only
         known = device if getattr(device, "index", None) is not None else None
         check_vector(given, "workspace", torch.uint8, nbytes, known)
         return given
-    return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
+    return alloc_on(stream, max(nbytes, 256), torch.uint8, device)
 
 
 def _run_ns(fname, wsfn, X, O, params, workspace, status, stream):
@@ -281,7 +291,7 @@ def _run_ns(fname, wsfn, X, O, params, workspace, status, stream):
     p = params or ns_params()
     with _on_device(Xb, Ob, stream=stream):
         need = wsfn(Xb, p)
-        ws = _workspace(need, Xb.device, workspace)
+        ws = _workspace(need, Xb.device, workspace, stream)
         check_vector(status, "status", torch.int32, 1, _dev(Xb))
         fn = getattr(L.lib(), fname)
         L.check(fname, fn(Xb.arr, Xb.dtype, Ob.arr, Ob.dtype, Xb.n, ctypes.byref(p),
@@ -368,7 +378,7 @@ def dion_lowrank_step(M, G, Q_state, W, params, scale=None, workspace=None,
     check_vector(status, "status", torch.int32, 1, _dev(Mb))
     with _on_device(Mb, Gb, Qb, Wb, stream=stream):
         need = dion_workspace_bytes(Mb, params, Qb)
-        ws = _workspace(need, Mb.device, workspace)
+        ws = _workspace(need, Mb.device, workspace, stream)
         L.check("dion_lowrank_step", L.lib().dion_lowrank_step_stats(
             Mb.arr, Gb.arr, Gb.dtype, Qb.arr, Wb.arr, Wb.dtype, Mb.n,
             ctypes.byref(params), sc, ctypes.c_void_p(ws.data_ptr()), ws.numel(),
@@ -382,7 +392,11 @@ def dion_effective_rank(sigma: torch.Tensor, ranks: Sequence[int],
     n = len(ranks)
     check_vector(sigma, "sigma", torch.float32, sum(int(r) for r in ranks))
     if erank is None:
-        erank = torch.empty(max(n, 1), dtype=torch.float32, device=sigma.device)
+        if stream is not None and stream.device != sigma.device:
+            raise ValueError(f"the stream is on {stream.device}, sigma on {sigma.device}")
+        erank = alloc_on(stream, max(n, 1), torch.float32, sigma.device)
+        if stream is not None:  # the caller reads it on its own stream
+            erank.record_stream(torch.cuda.current_stream(sigma.device))
     check_vector(erank, "erank", torch.float32, n, sigma.device)
     rk = (ctypes.c_int * max(n, 1))(*[int(r) for r in ranks])
     with _on_device(stream=stream, tensors=(sigma, erank)):

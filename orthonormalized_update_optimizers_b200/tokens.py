@@ -17,7 +17,7 @@ from typing import Optional, Sequence, Union
 import torch
 
 from . import _lib as L
-from .binding import MatBatch
+from .binding import MatBatch, alloc_on
 
 __all__ = [
     "int8_empty", "quantize_int8", "quantize_int8_workspace_bytes", "int8_matmul", "rms_norm", "rms_norm_backward",
@@ -112,16 +112,20 @@ def _scale(t: torch.Tensor, name: str, dev: int, rows: int) -> bytes:
     return _ptr_bytes(_vec(t, name, dev, rows))
 
 
+def _check_stream(stream, dev: int) -> None:
+    if stream is not None and stream.device.index != dev:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{dev}")
+
+
 def _workspace(need: int, given: Optional[torch.Tensor], dev: int, stream):
-    """(address, bytes) of a workspace: the caller's, or one allocated here
-    (the allocator keeps it for the stream that uses it)."""
+    """The caller's workspace, or one allocated here for the stream that uses
+    it: (tensor or None, address, bytes)."""
     if need == 0:
-        return None, 0
+        return None, None, 0
     if given is None:
-        given = torch.empty(need, dtype=torch.uint8, device=dev)
-        if stream is not None:
-            given.record_stream(stream)
-    return _vec(given, "workspace", dev, need, torch.uint8), given.numel()
+        _check_stream(stream, dev)
+        given = alloc_on(stream, need, torch.uint8, dev)
+    return given, _vec(given, "workspace", dev, need, torch.uint8), given.numel()
 
 
 _get_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
@@ -137,8 +141,7 @@ def _run(fname: str, dev: int, stream, *args) -> None:
     if stream is None:
         s = _raw_stream(dev)
     else:
-        if stream.device.index != dev:
-            raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{dev}")
+        _check_stream(stream, dev)
         s = stream.cuda_stream
     if _get_device() == dev:
         rc = fn(*args, s)
@@ -192,10 +195,10 @@ def quantize_int8(X: Tensors, Q: Tensors, scale: Tensors, transpose: bool = Fals
         dev, code = xs[0].get_device(), _code(xs[0], "X")
         x, q = _mats(xs, "X", dev), _mats(qs, "Q", dev, torch.int8)
         sc = _vecs(scale, "scale", dev, qs)
-    wp, wn = None, 0
+    ws, wp, wn = None, None, 0  # ws: kept until the launch
     if transpose:
-        wp, wn = _workspace(L.lib().quantize_int8_workspace_bytes(x, code, n, 1), workspace, dev,
-                            stream)
+        ws, wp, wn = _workspace(L.lib().quantize_int8_workspace_bytes(x, code, n, 1), workspace,
+                                dev, stream)
     _run("quantize_int8", dev, stream, x, code, q, sc, n, 1 if transpose else 0, wp, wn)
 
 
@@ -275,7 +278,7 @@ def rms_norm_backward(dY: torch.Tensor, H: torch.Tensor, weight: torch.Tensor,
     dy, h, dx = _mat(dY, "dY", dev), _mat(H, "H", dev), _mat(dX, "dX", dev)
     rows, cols = dY.shape
     w, rp = _weight(weight, dev, cols), _vec(rstd, "rstd", dev, rows)
-    dh = dwp = wp = None
+    dh = dwp = ws = wp = None  # ws: kept until the launch
     wn = 0
     if dH is not None:
         if dH.dtype is not dX.dtype:
@@ -283,7 +286,8 @@ def rms_norm_backward(dY: torch.Tensor, H: torch.Tensor, weight: torch.Tensor,
         dh = _mat(dH, "dH", dev)
     if dweight is not None:
         dwp = _vec(dweight, "dweight", dev, cols)
-        wp, wn = _workspace(rms_norm_backward_workspace_bytes(rows, cols), workspace, dev, stream)
+        ws, wp, wn = _workspace(rms_norm_backward_workspace_bytes(rows, cols), workspace, dev,
+                                stream)
     _run("rms_norm_backward", dev, stream, dy, _code(dY, "dY"), h, _code(H, "H"), w,
          _code(weight, "weight"), rp, dh, dx, _code(dX, "dX"), dwp, wp, wn)
 

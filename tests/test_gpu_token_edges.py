@@ -85,3 +85,37 @@ def test_rms_norm_rounds_ties_to_even(cols, dtype):
         w = torch.tensor(np.resize(x[a], cols), device=DEV).to(dtype)
         ouo.rms_norm(h, w, Q=got, scale=scale, eps=0.0)
         assert np.array_equal(to64(got), sign * np.resize(q[a], cols))
+
+
+# ------------------------------------------------------ workspaces and streams
+
+
+def test_workspace_of_another_stream_is_not_one_that_is_still_in_use():
+    """The current stream keeps writing to a buffer that the host has given
+    back; calls on another stream that take a workspace of that size."""
+    rows, cols = 4096, 2048
+    x = torch.randn((rows, cols), device=DEV).to(BF)
+    w, rstd = torch.ones(cols, device=DEV), torch.ones(rows, device=DEV)
+    q, sc = ouo.int8_empty(cols, rows), torch.empty(cols, device=DEV)
+    dx, dw = torch.empty_like(x), torch.empty(cols, device=DEV)
+
+    def run(**kw):
+        ouo.quantize_int8(x, q, sc, transpose=True, **kw)
+        ouo.rms_norm_backward(x, x, w, rstd, dx, dweight=dw, **kw)
+
+    run()
+    want = [t.clone() for t in (q, sc, dx, dw)]
+    sizes = (ouo.quantize_int8_workspace_bytes(x, True),
+             ouo.rms_norm_backward_workspace_bytes(rows, cols))
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(5):
+        held = [torch.empty(n, dtype=torch.uint8, device=DEV) for n in sizes]
+        for _ in range(200):
+            for t in held:
+                t.fill_(255)
+        del held, t
+        run(stream=s)
+        s.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip((q, sc, dx, dw), want))
+        torch.cuda.synchronize()
