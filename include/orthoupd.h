@@ -509,13 +509,17 @@ int rms_norm_backward(const ouo_mat* dY, int dy_dtype, const ouo_mat* H,
  * the vocabulary,
  *   loss_t = tau^2 sum_k p_k (log p_k - log q_{idx_k}),
  *   lse_t  = log sum_v exp(S_tv / tau)          (for the gradient).
- * Entries whose index is outside [0, V) or whose logit / tau is -inf do not count
+ * Entries whose index is outside [0, V) or whose logit is -inf do not count
  * (padding); a row without entries has loss 0 and lse 0.  An index that
  * appears twice counts twice.  Masked student logits (-inf or the type's
  * lowest value) have q = 0: the loss is infinite (very large) where the teacher has
  * weight there; a row whose logits are all masked is not meaningful.
  * idx: int32 matrix.  K <= OUO_DISTILL_MAX_ENTRIES, temperature tau in
- * [1e-3, 1e3].  Rows may be 0.
+ * [1e-3, 1e3].  Rows may be 0.  Logits are multiplied by the fp32 number
+ * nearest to 1 / tau.  The loss is off by about tau^2 1e-7 up to tau = 4, above
+ * that by tau 2^-20 times the logits' mean distance from the row's largest
+ * at most; lse is rounded to fp32, and so q of the gradient is off by
+ * 2^-24 |lse_t| of itself.
  *
  * distill_loss_backward -- dloss: gradient of each row's loss (device
  * float[rows]), lse from distill_loss:

@@ -37,9 +37,12 @@ struct DistillArgs {
   void* dS; int64_t ldds; int ds_bf16;
 };
 
+// R: as wide as the student's sum.  (In float64 at every temperature, the loss
+// of 4096 x 131072 takes 177 us instead of 172.)
+template <class R>
 struct Teacher {
-  float p[OUO_DISTILL_MAX_ENTRIES];    // probability
-  float lp[OUO_DISTILL_MAX_ENTRIES];   // its logarithm
+  R p[OUO_DISTILL_MAX_ENTRIES];      // probability
+  float v[OUO_DISTILL_MAX_ENTRIES];  // logit
   alignas(16) int idx[OUO_DISTILL_MAX_ENTRIES];
 };
 
@@ -55,8 +58,8 @@ __device__ __forceinline__ float block_fmax(float v, float* red) {
   return v;
 }
 
-template <int TH>
-__device__ __forceinline__ float block_fsum(float v, float* red) {
+template <int TH, class R>
+__device__ __forceinline__ R block_fsum(R v, R* red) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
@@ -68,19 +71,21 @@ __device__ __forceinline__ float block_fsum(float v, float* red) {
 }
 
 // The row's teacher entries in shared memory: idx = -1 for one that does not
-// count (index outside the vocabulary, logit -inf).  False if none counts.
-// red: two sets of words for the two reductions.
-template <int TH>
-__device__ __forceinline__ bool teacher_probs(const DistillArgs& a, int64_t row, Teacher& t,
-                                              float (*red)[TH / 32]) {
+// count (index outside the vocabulary, logit -inf); the largest logit and the
+// sum of the exponentials.  False if none counts.  The largest logit is
+// subtracted before the division by tau: what is divided is small where it
+// matters, and finite.
+template <int TH, class R>
+__device__ __forceinline__ bool teacher_probs(const DistillArgs& a, int64_t row, Teacher<R>& t,
+                                              float* redm, R* redz, float* largest, R* norm) {
   float m = kLowest;
   int some = 0;
   for (int k = threadIdx.x; k < a.K; k += TH) {
     int i = a.I[row * a.ldi + k];
-    const float v = ld1(a.T, row * a.ldt + k, a.t_bf16) * a.inv_tau;
+    const float v = ld1(a.T, row * a.ldt + k, a.t_bf16);
     if (i < 0 || i >= a.V || v == -INFINITY) i = -1;
     t.idx[k] = i;
-    t.lp[k] = v;
+    t.v[k] = v;
     if (i >= 0) {
       m = fmaxf(m, v);
       some = 1;
@@ -91,19 +96,15 @@ __device__ __forceinline__ bool teacher_probs(const DistillArgs& a, int64_t row,
     if (k < OUO_DISTILL_MAX_ENTRIES) t.idx[k] = -1;
   }
   if (__syncthreads_or(some) == 0) return false;
-  m = block_fmax<TH>(m, red[0]);
-  float z = 0.f;
+  *largest = m = block_fmax<TH>(m, redm);
+  R z = 0;
   for (int k = threadIdx.x; k < a.K; k += TH) {
-    t.lp[k] -= m;
-    t.p[k] = t.idx[k] >= 0 ? expf(t.lp[k]) : 0.f;
+    t.p[k] = t.idx[k] >= 0 ? exp(((R)t.v[k] - (R)m) * (R)a.inv_tau) : (R)0;
     z += t.p[k];
   }
-  z = block_fsum<TH>(z, red[1]);
-  const float lz = logf(z), iz = 1.f / z;
-  for (int k = threadIdx.x; k < a.K; k += TH) {  // the thread's own entries
-    t.lp[k] -= lz;
-    t.p[k] *= iz;
-  }
+  *norm = z = block_fsum<TH>(z, redz);
+  const R iz = 1 / z;
+  for (int k = threadIdx.x; k < a.K; k += TH) t.p[k] *= iz;  // the thread's own entries
   return true;
 }
 
@@ -122,23 +123,25 @@ __device__ __forceinline__ Run split_run(const char* row, int es, int64_t j0, in
 // Running maximum (of the raw logits) and sum of exponentials of what a
 // thread has seen; c = log2(e) / tau turns logits into exponents of two.
 struct Soft {
-  float m, z;
-  __device__ __forceinline__ void raise(float mn, float c) {
+  using Z = float;
+  float m = kLowest, z = 0.f, inv, c;
+  __host__ __device__ explicit Soft(float inv_tau) : inv(inv_tau), c(inv_tau * kLog2e) {}
+  __device__ __forceinline__ void raise(float mn) {
     if (mn > m) {
       z *= ex2((m - mn) * c);
       m = mn;
     }
   }
-  __device__ __forceinline__ void add1(float v, float c) {
-    raise(v, c);
+  __device__ __forceinline__ void add1(float v) {
+    raise(v);
     z += ex2((v - m) * c);
   }
   template <int N>
-  __device__ __forceinline__ void add(const float (&v)[N], float c) {
+  __device__ __forceinline__ void add(const float (&v)[N]) {
     float mn = v[0];
 #pragma unroll
     for (int i = 1; i < N; ++i) mn = fmaxf(mn, v[i]);
-    raise(mn, c);
+    raise(mn);
     float s0 = 0.f, s1 = 0.f;
 #pragma unroll
     for (int i = 0; i < N; i += 2) {
@@ -147,19 +150,89 @@ struct Soft {
     }
     z += s0 + s1;
   }
+  __device__ __forceinline__ float sum() const { return z; }
+  // exp((x - y) / tau)
+  __device__ __forceinline__ float ratio(float x, float y) const { return ex2((x - y) * c); }
 };
+
+// The same for high temperatures: an error of 1e-7 in the sum is tau^2 times
+// that in the loss, while the loss itself does not grow with tau.  There all
+// exponentials are near 1, and what is summed (in float64) is their distance
+// from it, e^d - 1 with d = (x - m) / tau, each off by a few 2^-24 |d| only: the
+// loss is off by some tau 2^-22 times the logits' mean distance from their
+// maximum.  m follows the maximum only where d would pass 1.
+struct FineSoft {
+  using Z = double;
+  float m = kLowest, inv;
+  int n = 0;
+  double e = 0.0;
+  __host__ __device__ explicit FineSoft(float inv_tau) : inv(inv_tau) {}
+  __device__ __forceinline__ void raise(float mn) {
+    if ((mn - m) * inv > 1.f || n == 0) {
+      if (n) e += (e + n) * expm1(((double)m - (double)mn) * inv);
+      m = fmaxf(mn, kLowest);
+    }
+  }
+  // Taylor's series to d^10, whose rest is below 2^-24 of the value at |d| = 1
+  __device__ __forceinline__ float dist(float v) const {
+    const float d = (v - m) * inv;
+    float r = 1.f / 3628800;
+    r = fmaf(r, d, 1.f / 362880);
+    r = fmaf(r, d, 1.f / 40320);
+    r = fmaf(r, d, 1.f / 5040);
+    r = fmaf(r, d, 1.f / 720);
+    r = fmaf(r, d, 1.f / 120);
+    r = fmaf(r, d, 1.f / 24);
+    r = fmaf(r, d, 1.f / 6);
+    r = fmaf(r, d, 0.5f);
+    r = fmaf(d * d, r, d);
+    return d < -1.f ? ex2(d * kLog2e) - 1.f : r;  // (a NaN stays one)
+  }
+  __device__ __forceinline__ void add1(float v) {
+    raise(v);
+    e += (double)dist(v);
+    ++n;
+  }
+  template <int N>
+  __device__ __forceinline__ void add(const float (&v)[N]) {
+    float mn = v[0];
+#pragma unroll
+    for (int i = 1; i < N; ++i) mn = fmaxf(mn, v[i]);
+    raise(mn);
+    float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+      s0 += dist(v[i]);
+      s1 += dist(v[i + 1]);
+    }
+    e += (double)(s0 + s1);
+    n += N;
+  }
+  __device__ __forceinline__ double sum() const { return (double)n + e; }
+  __device__ __forceinline__ double ratio(float x, float y) const {
+    return exp(((double)x - (double)y) * inv);
+  }
+};
+
+__device__ __forceinline__ float ld_cluster(uint32_t addr, float) { return ptx::ld_cluster_float(addr); }
+__device__ __forceinline__ double ld_cluster(uint32_t addr, double) {
+  return __hiloint2double(ptx::ld_cluster_int(addr + 4), ptx::ld_cluster_int(addr));
+}
 
 // Bound by HBM: 4096 x 131072 bf16 in 171 us, 6.3 TB/s (191 without the prefetch).
 // One row per cluster: its CTAs divide the vocabulary and join their maxima
 // and sums through distributed shared memory (one CTA: no join).
-template <int BF, int TH>
+template <int BF, int TH, class SOFT>
 __global__ void __launch_bounds__(TH, 1024 / TH)
 distill_kernel(const __grid_constant__ DistillArgs a) {
   constexpr int kU = BF ? 4 : 2;  // chunks of 8 in flight per thread
-  __shared__ Teacher t;
-  __shared__ float red[4][TH / 32];
+  using Z = typename SOFT::Z;
+  __shared__ Teacher<Z> t;
+  __shared__ float red[2][TH / 32];
   __shared__ double redd[TH / 32];
-  __shared__ float join[2];
+  __shared__ Z redz[2][TH / 32];
+  __shared__ float joinm;
+  __shared__ Z joinz;
   uint32_t nct;
   asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(nct));
   const uint32_t rank = nct > 1 ? ptx::cluster_ctarank() : 0u;
@@ -169,8 +242,7 @@ distill_kernel(const __grid_constant__ DistillArgs a) {
   const int64_t j0 = rank * per < a.V ? rank * per : a.V;
   const int64_t j1 = j0 + per < a.V ? j0 + per : a.V;
   const Run r = split_run(s, BF ? 2 : 4, j0, j1);
-  const float c = a.inv_tau * kLog2e;
-  Soft f{kLowest, 0.f};
+  SOFT f(a.inv_tau);
   int64_t j = r.ja + 8 * threadIdx.x;
   // kU chunks at a time, the next ones on their way while these are summed (the
   // first ones while the teacher's entries are)
@@ -187,7 +259,9 @@ distill_kernel(const __grid_constant__ DistillArgs a) {
   auto whole = [&](int64_t at) { return at + 8 * TH * (kU - 1) < r.jb; };
   uint4 cur[kN];
   if (whole(j)) fetch(cur, j);
-  const bool any = teacher_probs<TH>(a, row, t, red);  // the same in every CTA of the cluster
+  float tm;
+  Z tz;
+  const bool any = teacher_probs<TH>(a, row, t, red[0], redz[0], &tm, &tz);  // as in the whole cluster
   if (!any) {
     if (threadIdx.x == 0 && rank == 0) {
       a.loss[row] = 0.f;
@@ -198,7 +272,7 @@ distill_kernel(const __grid_constant__ DistillArgs a) {
   // the logit of the thread's first entry, needed last
   float at_entry = 0.f;
   if (threadIdx.x < a.K && t.idx[threadIdx.x] >= 0) at_entry = ld1(s, t.idx[threadIdx.x], BF);
-  if (j0 + threadIdx.x < r.ja) f.add1(ld1(s, j0 + threadIdx.x, BF), c);
+  if (j0 + threadIdx.x < r.ja) f.add1(ld1(s, j0 + threadIdx.x, BF));
   while (whole(j)) {
     uint4 next[kN];
     if (whole(j + kStep)) fetch(next, j + kStep);
@@ -214,7 +288,7 @@ distill_kernel(const __grid_constant__ DistillArgs a) {
         v[4] = __uint_as_float(y.x); v[5] = __uint_as_float(y.y);
         v[6] = __uint_as_float(y.z); v[7] = __uint_as_float(y.w);
       }
-      f.add(v, c);
+      f.add(v);
     }
 #pragma unroll
     for (int i = 0; i < kN; ++i) cur[i] = next[i];
@@ -223,58 +297,63 @@ distill_kernel(const __grid_constant__ DistillArgs a) {
   for (; j < r.jb; j += 8 * TH) {
     float v[8];
     ld8(s, j, BF, v);
-    f.add(v, c);
+    f.add(v);
   }
-  if (r.jb + threadIdx.x < j1) f.add1(ld1(s, r.jb + threadIdx.x, BF), c);
+  if (r.jb + threadIdx.x < j1) f.add1(ld1(s, r.jb + threadIdx.x, BF));
 
-  float M = block_fmax<TH>(f.m, red[2]);
-  float Z = block_fsum<TH>(f.z * ex2((f.m - M) * c), red[3]);
+  float M = block_fmax<TH>(f.m, red[1]);
+  Z sum = block_fsum<TH>(f.sum() * f.ratio(f.m, M), redz[1]);
   if (nct > 1) {
     if (threadIdx.x == 0) {
-      join[0] = M;
-      join[1] = Z;
+      joinm = M;
+      joinz = sum;
     }
     __syncwarp();
     ptx::cluster_sync();
-    float m[8], z[8], mm = kLowest;
+    float m[8], mm = kLowest;
+    Z z[8];
 #pragma unroll
     for (int p = 0; p < 8; ++p) {
       m[p] = kLowest;
-      z[p] = 0.f;
+      z[p] = 0;
       if (p < (int)nct) {
-        m[p] = ptx::ld_cluster_float(ptx::mapa(ptx::smem_u32(&join[0]), p));
-        z[p] = ptx::ld_cluster_float(ptx::mapa(ptx::smem_u32(&join[1]), p));
+        m[p] = ptx::ld_cluster_float(ptx::mapa(ptx::smem_u32(&joinm), p));
+        z[p] = ld_cluster(ptx::mapa(ptx::smem_u32(&joinz), p), z[p]);
       }
       mm = fmaxf(mm, m[p]);
     }
-    Z = 0.f;
+    sum = 0;
 #pragma unroll
-    for (int p = 0; p < 8; ++p) Z += z[p] * ex2((m[p] - mm) * c);
+    for (int p = 0; p < 8; ++p)
+      if (p < (int)nct) sum += z[p] * f.ratio(m[p], mm);
     M = mm;
     __syncwarp();
     ptx::cluster_sync();  // everyone has read everyone's
     if (rank != 0) return;
   }
   // The few terms of the loss in float64: log p - log q cancels where the
-  // student is near the teacher.
-  const double lse = (double)M * (double)a.inv_tau + log((double)Z);
+  // student is near the teacher.  With both maxima and normalizers set apart,
+  //   sum_k p_k (log p_k - log q_k) = sum_k p_k (t_k - tm - (s_k - M)) / tau + log(sum / tz)
   double acc = 0.0;
   for (int k = threadIdx.x; k < a.K; k += TH) {
     const int i = t.idx[k];
-    const float p = t.p[k];
-    if (i < 0 || p == 0.f) continue;  // p = 0 also where the student's logit is -inf
+    const double p = t.p[k];
+    // below fp32's range p is 0, also where the student's logit is -inf
+    if (i < 0 || (float)p == 0.f) continue;
     const float x = k == threadIdx.x ? at_entry : ld1(s, i, BF);
-    acc += (double)p * ((double)t.lp[k] - ((double)(x * a.inv_tau) - lse));
+    acc += p * (((double)t.v[k] - (double)tm) - ((double)x - (double)M));
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
   if ((threadIdx.x & 31) == 0) redd[threadIdx.x >> 5] = acc;
   __syncthreads();
+  const double inv = (double)a.inv_tau;
   if (threadIdx.x == 0) {
     for (int w = 1; w < TH / 32; ++w) acc += redd[w];
-    a.loss[row] = (float)((double)a.tau * (double)a.tau * acc);
-    a.lse[row] = (float)lse;
+    const double kl = acc * inv + log((double)sum / (double)tz);
+    a.loss[row] = (float)((double)a.tau * (double)a.tau * kl);
   }
+  if (threadIdx.x == 32) a.lse[row] = (float)((double)M * inv + log((double)sum));
 }
 
 // Every CTA writes one segment of one row.  Bound by HBM: 4096 x 131072 bf16 in
@@ -283,7 +362,7 @@ template <int BF, int TH>
 __global__ void __launch_bounds__(TH, 1024 / TH)
 distill_bwd_kernel(const __grid_constant__ DistillArgs a, int64_t seg, int segs) {
   constexpr int kU = BF ? 4 : 2;
-  __shared__ Teacher t;
+  __shared__ Teacher<float> t;
   __shared__ float sq[OUO_DISTILL_MAX_ENTRIES];
   __shared__ float red[2][TH / 32];
   const int64_t row = blockIdx.x / segs;
@@ -292,11 +371,13 @@ distill_bwd_kernel(const __grid_constant__ DistillArgs a, int64_t seg, int segs)
   const float g = a.dloss[row] * a.tau, lse = a.lse[row];
   const char* s = reinterpret_cast<const char*>(a.S) + row * a.lds * (BF ? 2 : 4);
   char* d = reinterpret_cast<char*>(a.dS) + row * a.ldds * (a.ds_bf16 ? 2 : 4);
-  const bool any = g != 0.f && teacher_probs<TH>(a, row, t, red);
+  float tm, tz;
+  const bool any = g != 0.f && teacher_probs<TH>(a, row, t, red[0], red[1], &tm, &tz);
   // chunks that are 16-byte pieces of both matrices
   Run r = split_run(s, BF ? 2 : 4, j0, j1);
   if (((uintptr_t)d + r.ja * (a.ds_bf16 ? 2 : 4)) & 15) r.ja = r.jb = j0;
-  auto prob = [&](float x) { return ex2((x * a.inv_tau - lse) * kLog2e); };
+  // x / tau is not rounded before lse, of its size, is taken from it
+  auto prob = [&](float x) { return ex2(fmaf(x, a.inv_tau, -lse) * kLog2e); };
   if (any) {
     // dS may be S itself: the entries' own probabilities are read first
     for (int k = threadIdx.x; k < a.K; k += TH) {
@@ -379,6 +460,12 @@ bool small_blocks(int64_t logits, int64_t ctas) {
   return logits <= 16384 || (ctas > 4 * num_sms() && ctas < 6 * num_sms());
 }
 
+// Above it the loss sums with FineSoft.  A loss of 0.045 over 1000 logits, the
+// teacher having all of them: 6e-5 of it off at tau = 4 with Soft, at tau = 8 /
+// 100 / 1000 1e-6 / 2e-5 / 2e-4 with FineSoft (with Soft 2e-4 and more).  4096 x
+// 131072 bf16: 171 us with Soft, 350-365 with FineSoft, bound by instructions.
+constexpr float kFineTau = 4.f;
+
 int check_distill(const ouo_mat* S, int s_dtype, const ouo_mat* teacher, int t_dtype,
                   const ouo_mat* idx, float temperature) {
   if (!S || !teacher || !idx)
@@ -449,8 +536,12 @@ int distill_loss(const ouo_mat* S, int s_dtype, const ouo_mat* teacher, int t_dt
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  auto kern = a.s_bf16 ? (small ? distill_kernel<1, 128> : distill_kernel<1, 256>)
-                       : (small ? distill_kernel<0, 128> : distill_kernel<0, 256>);
+  auto choose = [&](auto soft) {
+    using S = decltype(soft);
+    return a.s_bf16 ? (small ? distill_kernel<1, 128, S> : distill_kernel<1, 256, S>)
+                    : (small ? distill_kernel<0, 128, S> : distill_kernel<0, 256, S>);
+  };
+  auto kern = temperature > kFineTau ? choose(FineSoft(1.f)) : choose(Soft(1.f));
   OUO_CHECK_CUDA(cudaLaunchKernelEx(&cfg, kern, a));
   OUO_CHECK_LAUNCH();
   return OUO_OK;

@@ -5,12 +5,14 @@ import pytest
 import torch
 
 import orthonormalized_update_optimizers_b200 as ouo
+from oracle import tokens as ot
 
 from ._util import to64
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
 BF, F32 = torch.bfloat16, torch.float32
+U32 = 2.0 ** -24  # half a step of fp32
 
 
 # ------------------------------------------------------ ties of the rounding
@@ -119,3 +121,123 @@ def test_workspace_of_another_stream_is_not_one_that_is_still_in_use():
         s.synchronize()
         assert all(torch.equal(a, b) for a, b in zip((q, sc, dx, dw), want))
         torch.cuda.synchronize()
+
+
+# ------------------------------------------- temperatures far from the usual
+
+
+def _near_teacher(rows, vocab, dtype, seed):
+    """Logits, and a teacher that has every entry of the vocabulary, near them."""
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed)
+    s = torch.randn((rows, vocab), generator=g, device=DEV).to(dtype)
+    idx = torch.stack([torch.randperm(vocab, generator=g, device=DEV) for _ in range(rows)])
+    t = s.float().gather(1, idx) + 0.3 * torch.randn((rows, vocab), generator=g, device=DEV)
+    return s, t, idx.to(torch.int32)
+
+
+TAUS = [1e-3, 1e-2, 0.3, 1.0, 4.0, 4.5, 20.0, 100.0, 1000.0]
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("tau", TAUS)
+@pytest.mark.parametrize("vocab", [10, 1000])
+def test_distill_loss_keeps_its_digits_at_any_temperature(vocab, tau, dtype):
+    s, t, idx = _near_teacher(4, vocab, dtype, 3)
+    loss, lse = torch.empty(4, device=DEV), torch.empty(4, device=DEV)
+    ouo.distill_loss(s, t, idx, loss, lse, temperature=tau)
+    # the operator divides by tau as a product with the fp32 number nearest to 1 / tau
+    inv = float(np.float32(1) / np.float32(tau))
+    le, ze = ot.distill_loss(to64(s), to64(t), idx.cpu().numpy(), 1 / inv)
+    le = le * (float(np.float32(tau)) * inv) ** 2
+    x = to64(s)
+    d = (x.max(1, keepdims=True) - x) * inv
+    Z = np.exp(-d).sum(1)
+    if tau <= 4:
+        # the exponential: 2 ulp, its argument three roundings; a thread's sum
+        # of vocab / 128 terms, in eights, and the block's
+        eps = 4 * U32 + 3 * U32 * (d * np.exp(-d)).sum(1) / Z + (vocab / 1024 + 24) * U32
+        # the teacher's: as much in the sum, and in each p (all of them cover
+        # the vocabulary; the logits are 0.3 apart, five times that at most)
+        both = 2 * eps + (eps + 4 * U32 + 3 * U32 * d.max(1)) * 2 * 5 * 0.3 * inv
+    else:
+        # what is summed is within 14 roundings of e^d - 1, at most 1.8 |d|: two
+        # in d, four in the series (or the exponential and the 1), four in sums of
+        # eight; m may be below the logit, by d = 1 at most.  The teacher in float64.
+        both = eps = 14 * U32 * np.maximum(d, np.minimum(1, d.max(1, keepdims=True))).sum(1) / Z
+    assert np.all(np.abs(to64(loss) - le) <= tau * tau * both + 2 * U32 * np.abs(le))
+    assert np.all(np.abs(to64(lse) - ze) <= eps + 2 * U32 * np.abs(ze))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("tau", TAUS)
+def test_distill_gradient_keeps_its_digits_at_any_temperature(tau, dtype):
+    vocab = 1000
+    s, t, idx = _near_teacher(4, vocab, dtype, 4)
+    loss, lse, dl = (torch.ones(4, device=DEV) for _ in range(3))
+    ouo.distill_loss(s, t, idx, loss, lse, temperature=tau)
+    ds = torch.empty((4, vocab), device=DEV)
+    ouo.distill_loss_backward(s, t, idx, lse, dl, ds, temperature=tau)
+    inv = float(np.float32(1) / np.float32(tau))
+    e = ot.distill_grad(to64(s), to64(t), idx.cpu().numpy(), to64(lse), to64(dl), 1 / inv)
+    e = e * float(np.float32(tau)) * inv
+    x = to64(s) * inv - to64(lse)[:, None]
+    q = np.exp(x)
+    T = np.empty_like(x)
+    np.put_along_axis(T, idx.cpu().numpy().astype(np.int64), to64(t), 1)
+    d = (T.max(1, keepdims=True) - T) * inv
+    p = np.exp(-d) / np.exp(-d).sum(1, keepdims=True)
+    # q: a fused product, log2(e) (2), the exponential (2 ulp); p: d (2), the
+    # exponential (2), the sum of 1000 / 128 terms and the block's, 1 / z (2)
+    eq = (4 * np.abs(x) + 4) * U32 * q
+    ep = (2 * d + 3 * np.sum(p * d, 1, keepdims=True) + 8 + 8 + 12) * U32 * p
+    # the difference and two products; tiny probabilities may be flushed
+    tol = tau * (eq + ep + 2.0 ** -126) + 4 * U32 * np.abs(e)
+    assert np.all(np.abs(to64(ds) - e) <= tol)
+
+
+@pytest.mark.parametrize("tau", [0.25, 0.7, 1.0, 8.0])
+def test_distill_teacher_of_lowest_values_at_any_temperature(tau):
+    """Entries that all have the lowest value count, equally, although the
+    quotient by the temperature is not finite."""
+    s = torch.randn((2, 50), generator=torch.Generator(DEV).manual_seed(2), device=DEV)
+    t = torch.full((2, 4), torch.finfo(F32).min, device=DEV)
+    t[1, 0] = 1.0
+    idx = torch.tensor([[1, 2, 3, 4]] * 2, device=DEV, dtype=torch.int32)
+    loss, lse = torch.empty(2, device=DEV), torch.empty(2, device=DEV)
+    ouo.distill_loss(s, t, idx, loss, lse, temperature=tau)
+    near = np.array([[0.0] * 4, [1.0] + [-1e30] * 3])
+    le, ze = ot.distill_loss(to64(s), near, idx.cpu().numpy(), tau)
+    # the tolerance of the masked rows at temperature 1, times tau^2
+    assert np.abs(to64(loss) - le).max() <= 200 * U32 * max(1.0, tau * tau)
+    ds, dl = torch.empty_like(s), torch.ones(2, device=DEV)
+    ouo.distill_loss_backward(s, t, idx, lse, dl, ds, temperature=tau)
+    e = ot.distill_grad(to64(s), near, idx.cpu().numpy(), to64(lse), np.ones(2), tau)
+    assert np.abs(to64(ds) - e).max() <= 200 * U32 * max(1.0, tau)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("rows,vocab", [(2, 131072), (33, 4099), (700, 64), (300, 50001)])
+def test_distill_high_temperature_over_shapes(rows, vocab, dtype):
+    """Clusters, odd rows and short ones; masked and skipped entries."""
+    tau, k = 50.0, 32
+    g = torch.Generator(DEV).manual_seed(5)
+    s = (torch.randn((rows, vocab), generator=g, device=DEV) * 3).to(dtype)
+    s[0, 5:9] = -float("inf")
+    s[1, 5:9] = torch.finfo(dtype).min
+    t = torch.randn((rows, k), generator=g, device=DEV)
+    idx = torch.randint(9, vocab, (rows, k), generator=g, device=DEV).to(torch.int32)
+    if rows > 2:
+        idx[2] = -1
+    loss, lse = torch.empty(rows, device=DEV), torch.empty(rows, device=DEV)
+    ouo.distill_loss(s, t, idx, loss, lse, temperature=tau)
+    inv = float(np.float32(1) / np.float32(tau))
+    le, ze = ot.distill_loss(to64(s), to64(t), idx.cpu().numpy(), 1 / inv)
+    le = le * (float(np.float32(tau)) * inv) ** 2
+    x = to64(s)
+    d = np.minimum((x.max(1, keepdims=True) - x) * inv, 1e3)
+    # as above; where logits are masked, e^d - 1 is -1
+    far = np.minimum(1, np.where(d < 1e3, d, 0).max(1, keepdims=True))
+    eps = 14 * U32 * np.minimum(np.maximum(d, far), 2.0).sum(1) / np.exp(-d).sum(1)
+    assert np.all(np.abs(to64(loss) - le) <= tau * tau * eps + 2 * U32 * np.abs(le))
+    assert np.all(np.abs(to64(lse) - ze) <= eps + 2 * U32 * np.abs(ze))
