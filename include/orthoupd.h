@@ -74,6 +74,7 @@ extern "C" {
 
 /* limits of the token-matrix calls */
 #define OUO_INT8_MAX_DEPTH 131071     /* int8_matmul: depth whose sums fit in 32 bits */
+#define OUO_INT8_MAX_DEEP 1047552     /* int8_matmul_deep                             */
 #define OUO_DISTILL_MAX_ENTRIES 1024  /* distill_loss: teacher entries of a row        */
 
 /* momentum modes */
@@ -465,11 +466,19 @@ int quantize_int8(const ouo_mat* X, int x_dtype, const ouo_mat* Q,
  *   Y  = int8_matmul(q(X), q(W)),  dX = int8_matmul(q(dY), q^T(W)),
  *   dW = int8_matmul(q^T(dY), q^T(X)),   q^T = quantize_int8 transposed,
  * and dW is the G of dion_momentum_update.
+ *
+ * int8_matmul_deep -- the same, for K <= OUO_INT8_MAX_DEEP: above
+ * OUO_INT8_MAX_DEPTH the sums, exact too, are held in 64 bits (dX of a
+ * vocabulary's head has the vocabulary as its depth).
  */
 int int8_matmul(const ouo_mat* A, const float* const* a_scale,
                 const ouo_mat* B, const float* const* b_scale,
                 const ouo_mat* D, int d_dtype, int nmat, int* dev_status,
                 void* stream);
+int int8_matmul_deep(const ouo_mat* A, const float* const* a_scale,
+                     const ouo_mat* B, const float* const* b_scale,
+                     const ouo_mat* D, int d_dtype, int nmat, int* dev_status,
+                     void* stream);
 
 /*
  * rms_norm -- per row t:

@@ -33,6 +33,7 @@ OUO_STATUS_TIMEOUT = 1
 OUO_STATUS_BREAKDOWN = 2
 OUO_MAX_RESTARTS = 8
 OUO_INT8_MAX_DEPTH = 131071
+OUO_INT8_MAX_DEEP = 1047552
 OUO_DISTILL_MAX_ENTRIES = 1024
 OUO_NOALLOC_SCRATCH_BYTES = 64 * 1024 * 1024
 
@@ -46,7 +47,8 @@ EXPORTED = (
     "dion_workspace_bytes", "dion_lowrank_step", "dion_workspace_bytes_ranks",
     "dion_lowrank_step_stats", "dion_effective_rank", "dion_shard_workspace_bytes",
     "dion_shard_red_floats", "dion_shard_project", "dion_shard_orth1", "dion_shard_orth2",
-    "dion_shard_update", "quantize_int8_workspace_bytes", "quantize_int8", "int8_matmul", "rms_norm",
+    "dion_shard_update", "quantize_int8_workspace_bytes", "quantize_int8", "int8_matmul",
+    "int8_matmul_deep", "rms_norm",
     "rms_norm_backward_workspace_bytes", "rms_norm_backward", "distill_loss",
     "distill_loss_backward",
 )
@@ -128,6 +130,7 @@ _PROTOS = {
     "quantize_int8_workspace_bytes": (_SZ, [_P, _I, _I, _I]),
     "quantize_int8": (_I, [_P, _I, _P, _P, _I, _I, _P, _SZ, _P]),
     "int8_matmul": (_I, [_P, _P, _P, _P, _P, _I, _I, _P, _P]),
+    "int8_matmul_deep": (_I, [_P, _P, _P, _P, _P, _I, _I, _P, _P]),
     "rms_norm": (_I, [_P, _I, _P, _P, _I, _P, _I, _F, _P, _I, _P, _P, _P, _P]),
     "rms_norm_backward_workspace_bytes": (_SZ, [_I64, _I64]),
     "rms_norm_backward": (_I, [_P, _I, _P, _I, _P, _I, _P, _P, _P, _I, _P, _P, _SZ, _P]),

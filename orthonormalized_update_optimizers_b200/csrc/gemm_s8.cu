@@ -15,6 +15,9 @@
 //     and by some 4 us of set-up and join: 16 x 14336 x 4096 in 14.7 us.
 // Matrices whose rows do not start on 16-byte boundaries cannot be read by the
 // TMA; they take a CUDA-core kernel (dp4a).
+// int8_matmul_deep, for depths whose sums leave 32 bits, cuts K into pieces that
+// do not and adds those in 64 bits: the split kernel's eight CTAs, where it
+// joins them, or in registers.
 #include <cuda.h>
 
 #include <cstring>
@@ -28,6 +31,10 @@ namespace {
 
 // CUDA cores: 64 x 64 tile per block, 32 bytes of K per step, 4 x 4 outputs
 // per thread, four products per dp4a.  Takes any row pitch and alignment.
+// DEEP: 32-bit sums of kSimtPiece elements are added in 64 bits.
+constexpr int64_t kSimtPiece = OUO_INT8_MAX_DEPTH / 32 * 32;
+
+template <int DEEP>
 __global__ void __launch_bounds__(256)
 s8_simt_kernel(const int8_t* A, int64_t lda, const int8_t* B, int64_t ldb, const float* as,
                const float* bs, void* D, int64_t ldd, int bf16, int64_t M, int64_t N, int64_t K,
@@ -36,7 +43,19 @@ s8_simt_kernel(const int8_t* A, int64_t lda, const int8_t* B, int64_t ldb, const
   const int64_t m0 = blockIdx.x / tiles_n * 64, n0 = blockIdx.x % tiles_n * 64;
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   int acc[4][4] = {};
+  long long wide[4][4] = {};
+  int64_t next = kSimtPiece;
   for (int64_t k0 = 0; k0 < K; k0 += 32) {
+    if (DEEP && k0 == next) {
+      next += kSimtPiece;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          wide[i][j] += acc[i][j];
+          acc[i][j] = 0;
+        }
+    }
     for (int e = threadIdx.x; e < 512; e += 256) {
       const int r = e >> 3, w = e & 7;
       int va = 0, vb = 0;
@@ -72,7 +91,8 @@ s8_simt_kernel(const int8_t* A, int64_t lda, const int8_t* B, int64_t ldb, const
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int64_t n = n0 + tx + 16 * j;
-      if (n < N) st1(D, m * ldd + n, (float)acc[i][j] * as[m] * bs[n], bf16);
+      const float sum = DEEP ? (float)(wide[i][j] + acc[i][j]) : (float)acc[i][j];
+      if (n < N) st1(D, m * ldd + n, sum * as[m] * bs[n], bf16);
     }
   }
 }
@@ -80,7 +100,8 @@ s8_simt_kernel(const int8_t* A, int64_t lda, const int8_t* B, int64_t ldb, const
 
 // MT tokens, one or two: a warp per row of B (per 4 for two tokens), 16 bytes a
 // lane and load, dp4a.  Bound by reading B; the tensor-core kernels' set-up (TMEM, barriers,
-// a pipeline to fill) costs more than these few products.
+// a pipeline to fill) costs more than these few products.  A lane's share of K,
+// a 32nd, fits in 32 bits at any depth; the lanes' sum is taken in two halves.
 constexpr int kVecThreads = 128;
 template <int MT>
 constexpr int kVecRows = MT == 1 ? 1 : 4;
@@ -135,9 +156,16 @@ s8_vec_kernel(const int8_t* A, int64_t lda, const int8_t* B, int64_t ldb, const 
   for (int r = 0; r < kR; ++r)
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
-      const int s = __reduce_add_sync(0xffffffffu, acc[r][m]);
+      float s;
+      if (K <= OUO_INT8_MAX_DEPTH) {
+        s = (float)__reduce_add_sync(0xffffffffu, acc[r][m]);
+      } else {
+        const int hi = __reduce_add_sync(0xffffffffu, acc[r][m] >> 16);
+        const int lo = __reduce_add_sync(0xffffffffu, acc[r][m] & 0xffff);
+        s = (float)((long long)hi * 65536 + lo);
+      }
       if (lane == r * MT + m && n0 + r < N)
-        st1(D, m * ldd + n0 + r, (float)s * as[m] * bs[n0 + r], bf16);
+        st1(D, m * ldd + n0 + r, s * as[m] * bs[n0 + r], bf16);
     }
 }
 
@@ -453,7 +481,9 @@ struct SplitCfg {
   static_assert((size_t)BN * 512 <= (size_t)kStages * kStage, "partial sums reuse the stages");
 };
 
-template <int BN, int NS /* CTAs of the cluster, which divide K */>
+// NS: CTAs of the cluster, which divide K.  DEEP: each one's sums fit in 32
+// bits, all together in 64.
+template <int BN, int NS, int DEEP>
 __global__ void __launch_bounds__(kSplitThreads)
 s8_split_kernel(const __grid_constant__ SplitArgs a) {
   using C = SplitCfg<BN>;
@@ -596,6 +626,7 @@ s8_split_kernel(const __grid_constant__ SplitArgs a) {
   __syncwarp();
   if (NS > 1) ptx::cluster_sync();
   else __syncthreads();
+  using Sum = std::conditional_t<DEEP, long long, int>;
   // Branched on the output's type once: a branch per element costs more than
   // the element (a 128 x 128 tile took 12,000 cycles to write).
   {
@@ -610,15 +641,15 @@ s8_split_kernel(const __grid_constant__ SplitArgs a) {
         E* d = reinterpret_cast<E*>(a.D) + (int64_t)first * a.ldd + r;
 #pragma unroll 4
         for (int j = warp; j < n; j += kSplitThreads / 32) {
-          int4 x = make_int4(0, 0, 0, 0);
+          Sum x[4] = {0, 0, 0, 0};
 #pragma unroll
           for (int p = 0; p < NS; ++p) {
             const int4 y = *reinterpret_cast<const int4*>(part + (p * kPer + j) * 128 + 4 * lane);
-            x.x += y.x; x.y += y.y; x.z += y.z; x.w += y.w;
+            x[0] += y.x; x[1] += y.y; x[2] += y.z; x[3] += y.w;
           }
           const float t = ts[j];
-          const float v[4] = {(float)x.x * t * s4.x, (float)x.y * t * s4.y, (float)x.z * t * s4.z,
-                              (float)x.w * t * s4.w};
+          const float v[4] = {(float)x[0] * t * s4.x, (float)x[1] * t * s4.y,
+                              (float)x[2] * t * s4.z, (float)x[3] * t * s4.w};
           E* o = d + (int64_t)j * a.ldd;
           if (wide) {
             if (BF) *reinterpret_cast<uint2*>(o) = make_uint2(pack2(v[0], v[1]), pack2(v[2], v[3]));
@@ -634,7 +665,7 @@ s8_split_kernel(const __grid_constant__ SplitArgs a) {
         const float s = rs[row];
         E* d = reinterpret_cast<E*>(a.D) + (int64_t)(r0 + row) * a.ldd + first;
         auto value = [&](int j) {
-          int x = 0;
+          Sum x = 0;
 #pragma unroll
           for (int p = 0; p < NS; ++p) x += part[(p * kPer + j) * 128 + row];
           return (float)x * s * ts[j];
@@ -794,11 +825,11 @@ int run_pair(const Product& p, cudaStream_t s) {
 }
 
 // t_rows: T is A (D's rows), R is B; else the other way round.
-template <int BN, int NS>
+template <int BN, int NS, int DEEP>
 int run_split(const Product& p, bool t_rows, cudaStream_t s) {
   using C = SplitCfg<BN>;
   static Once once;
-  OUO_TRY(once.smem((s8_split_kernel<BN, NS>), C::kSmem));
+  OUO_TRY(once.smem((s8_split_kernel<BN, NS, DEEP>), C::kSmem));
   SplitArgs a;
   memset(&a, 0, sizeof(a));
   const ouo_mat& R = t_rows ? p.B : p.A;
@@ -819,25 +850,27 @@ int run_split(const Product& p, bool t_rows, cudaStream_t s) {
   if (tiles * NS > 0x7fffffff) return set_error(OUO_ERR_UNSUPPORTED, "D: too many tiles");
   cudaLaunchAttribute attr[1];
   cudaLaunchConfig_t cfg = config((unsigned)(tiles * NS), kSplitThreads, C::kSmem, s, NS, attr);
-  OUO_CHECK_CUDA(cudaLaunchKernelEx(&cfg, s8_split_kernel<BN, NS>, a));
+  OUO_CHECK_CUDA(cudaLaunchKernelEx(&cfg, s8_split_kernel<BN, NS, DEEP>, a));
   OUO_CHECK_LAUNCH();
   return OUO_OK;
 }
 
 template <int BN>
 int run_split(const Product& p, bool t_rows, int nsplit, cudaStream_t s) {
+  if (p.A.cols > OUO_INT8_MAX_DEPTH) return run_split<BN, 8, 1>(p, t_rows, s);
   switch (nsplit) {
-    case 1: return run_split<BN, 1>(p, t_rows, s);
-    case 2: return run_split<BN, 2>(p, t_rows, s);
-    case 4: return run_split<BN, 4>(p, t_rows, s);
-    default: return run_split<BN, 8>(p, t_rows, s);
+    case 1: return run_split<BN, 1, 0>(p, t_rows, s);
+    case 2: return run_split<BN, 2, 0>(p, t_rows, s);
+    case 4: return run_split<BN, 4, 0>(p, t_rows, s);
+    default: return run_split<BN, 8, 0>(p, t_rows, s);
   }
 }
 
 int run_simt(const Product& p, cudaStream_t s) {
   const int64_t tn = ceil_div(p.D.cols, 64), tiles = ceil_div(p.D.rows, 64) * tn;
   if (tiles > 0x7fffffff) return set_error(OUO_ERR_UNSUPPORTED, "D: too many tiles");
-  s8_simt_kernel<<<(unsigned)tiles, 256, 0, s>>>(
+  auto kern = p.A.cols > OUO_INT8_MAX_DEPTH ? s8_simt_kernel<1> : s8_simt_kernel<0>;
+  kern<<<(unsigned)tiles, 256, 0, s>>>(
       (const int8_t*)p.A.ptr, p.A.ld, (const int8_t*)p.B.ptr, p.B.ld, p.as, p.bs, p.D.ptr, p.D.ld,
       p.bf16, p.D.rows, p.D.cols, p.A.cols, tn);
   OUO_CHECK_LAUNCH();
@@ -867,7 +900,7 @@ int product(const Product& p, cudaStream_t s) {
   // 4096 (64 tiles) against 20.5 in the split kernel, 17.1 against 15.8 at half
   // the rows (32 tiles).
   const int64_t sms = num_sms();
-  if (M > 128 && N > 128 && 3 * ceil_div(M, 256) * ceil_div(N, 256) >= sms) return run_pair(p, s);
+  if (K <= OUO_INT8_MAX_DEPTH && M > 128 && N > 128 && 3 * ceil_div(M, 256) * ceil_div(N, 256) >= sms) return run_pair(p, s);
   // T is the side with fewer rows, A unless B's rows are few.
   const bool t_rows = M <= N || N > 128;
   const int64_t T = t_rows ? M : N, R = t_rows ? N : M;
@@ -889,13 +922,12 @@ int product(const Product& p, cudaStream_t s) {
   }
 }
 
-}  // namespace
-}  // namespace ouo
+// Deepest product: eight CTAs' shares of whole stages, each with 32-bit sums.
+static_assert(OUO_INT8_MAX_DEEP == 8 * (OUO_INT8_MAX_DEPTH / 128 * 128), "eight CTAs' depth");
 
-extern "C" int int8_matmul(const ouo_mat* A, const float* const* a_scale, const ouo_mat* B,
-                           const float* const* b_scale, const ouo_mat* D, int d_dtype, int nmat,
-                           int* dev_status, void* stream) {
-  using namespace ouo;
+int matmul(int64_t deepest, const ouo_mat* A, const float* const* a_scale, const ouo_mat* B,
+           const float* const* b_scale, const ouo_mat* D, int d_dtype, int nmat, int* dev_status,
+           void* stream) {
   clear_error();
   if (nmat < 0 || nmat > OUO_MAX_BATCH)
     return set_error(OUO_ERR_INVALID_ARG, "nmat %d out of range", nmat);
@@ -912,10 +944,10 @@ extern "C" int int8_matmul(const ouo_mat* A, const float* const* a_scale, const 
     if (A[i].cols != B[i].cols)
       return set_error(OUO_ERR_INVALID_ARG, "A[%d] has %lld columns, B[%d] has %lld", i,
                        (long long)A[i].cols, i, (long long)B[i].cols);
-    if (A[i].cols > OUO_INT8_MAX_DEPTH)
+    if (A[i].cols > deepest)
       return set_error(OUO_ERR_UNSUPPORTED,
-                       "A[%d]: depth %lld above %d (the sums would leave 32 bits)", i,
-                       (long long)A[i].cols, OUO_INT8_MAX_DEPTH);
+                       "A[%d]: depth %lld above %lld (the sums would leave 32 bits)", i,
+                       (long long)A[i].cols, (long long)deepest);
     OUO_TRY(validate_shape(D[i], A[i].rows, B[i].rows, "D", i));
     OUO_TRY(validate_vec(a_scale[i], A[i].rows, 4, "a_scale"));
     OUO_TRY(validate_vec(b_scale[i], B[i].rows, 4, "b_scale"));
@@ -928,3 +960,24 @@ extern "C" int int8_matmul(const ouo_mat* A, const float* const* a_scale, const 
   }
   return OUO_OK;
 }
+
+}  // namespace
+}  // namespace ouo
+
+extern "C" {
+
+int int8_matmul(const ouo_mat* A, const float* const* a_scale, const ouo_mat* B,
+                const float* const* b_scale, const ouo_mat* D, int d_dtype, int nmat,
+                int* dev_status, void* stream) {
+  return ouo::matmul(OUO_INT8_MAX_DEPTH, A, a_scale, B, b_scale, D, d_dtype, nmat, dev_status,
+                     stream);
+}
+
+int int8_matmul_deep(const ouo_mat* A, const float* const* a_scale, const ouo_mat* B,
+                     const float* const* b_scale, const ouo_mat* D, int d_dtype, int nmat,
+                     int* dev_status, void* stream) {
+  return ouo::matmul(OUO_INT8_MAX_DEEP, A, a_scale, B, b_scale, D, d_dtype, nmat, dev_status,
+                     stream);
+}
+
+}  // extern "C"

@@ -206,13 +206,14 @@ def int8_matmul(A: Tensors, a_scale: Tensors, B: Tensors, b_scale: Tensors, D: T
                 status: Optional[torch.Tensor] = None, stream=None) -> None:
     """D <- diag(a_scale) (A B^T) diag(b_scale), A (M x K) and B (N x K) 8-bit
     integers as quantize_int8 writes them.  Tensors, or lists of equal
-    length."""
+    length.  Depths whose sums leave 32 bits go to int8_matmul_deep."""
     if isinstance(A, torch.Tensor) and isinstance(B, torch.Tensor) and isinstance(D, torch.Tensor):
         dev, n = A.get_device(), 1
         a, b = _mat(A, "A", dev, torch.int8), _mat(B, "B", dev, torch.int8)
         d, code = _mat(D, "D", dev), _code(D, "D")
         sa = _scale(a_scale, "a_scale", dev, A.shape[0])
         sb = _scale(b_scale, "b_scale", dev, B.shape[0])
+        depth = A.shape[1]
     else:
         As, Bs, Ds = _list(A), _list(B), _list(D)
         n = len(As)
@@ -224,8 +225,9 @@ def int8_matmul(A: Tensors, a_scale: Tensors, B: Tensors, b_scale: Tensors, D: T
         a, b = _mats(As, "A", dev, torch.int8), _mats(Bs, "B", dev, torch.int8)
         d, code = _mats(Ds, "D", dev), _code(Ds[0], "D")
         sa, sb = _vecs(a_scale, "a_scale", dev, As), _vecs(b_scale, "b_scale", dev, Bs)
+        depth = max(t.shape[1] for t in As)
     st = None if status is None else _vec(status, "status", dev, 1, torch.int32)
-    _run("int8_matmul", dev, stream, a, sa, b, sb, d, code, n, st)
+    _run("int8_matmul" if depth <= L.OUO_INT8_MAX_DEPTH else "int8_matmul_deep", dev, stream, a, sa, b, sb, d, code, n, st)
 
 
 def rms_norm(X: torch.Tensor, weight: torch.Tensor, Y: Optional[torch.Tensor] = None,

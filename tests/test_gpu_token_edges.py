@@ -241,3 +241,115 @@ def test_distill_high_temperature_over_shapes(rows, vocab, dtype):
     eps = 14 * U32 * np.minimum(np.maximum(d, far), 2.0).sum(1) / np.exp(-d).sum(1)
     assert np.all(np.abs(to64(loss) - le) <= tau * tau * eps + 2 * U32 * np.abs(le))
     assert np.all(np.abs(to64(lse) - ze) <= eps + 2 * U32 * np.abs(ze))
+
+
+# ------------------------------------------------ depths past sums of 32 bits
+
+
+def _ints(shape, seed, lo=-127, hi=127):
+    g = torch.Generator(DEV).manual_seed(seed)
+    return torch.randint(lo, hi + 1, shape, generator=g, device=DEV, dtype=torch.int8)
+
+
+def _exact_product(a, sa, b, sb):
+    """In float64, where these sums are exact."""
+    e = a.double() @ b.double().t()
+    assert e.abs().max() < 2 ** 53
+    return (e * sa.double()[:, None] * sb.double()).cpu().numpy()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("m,n,k", [
+    (1, 130, 131072), (2, 70, 152064), (5, 33, 131072), (30, 260, 200001), (64, 40, 131200),
+    (200, 300, 152064), (300, 100, 256000), (3, 7, 1047552), (130, 129, 131072)])
+@pytest.mark.parametrize("extreme", [False, True])
+def test_deep_product(m, n, k, dtype, extreme):
+    if extreme:  # every sum as large as it gets, or as small
+        a, b = ouo.int8_empty(m, k).fill_(-128), ouo.int8_empty(n, k).fill_(-128)
+        b[1::2].fill_(127)
+    else:
+        a = ouo.int8_empty(m, k).copy_(_ints((m, k), 1))
+        b = ouo.int8_empty(n, k).copy_(_ints((n, k), 2))
+    sa = torch.rand(m, device=DEV) + 0.1
+    sb = torch.rand(n, device=DEV) - 0.5
+    d = torch.full((m, n + 5), 77.0, dtype=dtype, device=DEV)
+    st = torch.zeros(1, dtype=torch.int32, device=DEV)
+    ouo.int8_matmul(a, sa, b, sb, d[:, :n], status=st)
+    e = _exact_product(a, sa, b, sb)
+    tol = (1 + {BF: 2.0 ** -8, F32: U32}[dtype]) * (1 + U32) ** 3 - 1
+    assert np.all(np.abs(to64(d[:, :n]) - e) <= tol * np.abs(e))
+    assert (d[:, n:] == 77).all() and st.item() == 0
+
+
+@pytest.mark.parametrize("m,n,k", [(1, 9, 131073), (70, 66, 131072), (5, 130, 300001)])
+@pytest.mark.parametrize("extreme", [False, True])
+def test_deep_product_of_unaligned_rows(m, n, k, extreme):
+    def rows(r, seed):
+        if extreme:
+            return torch.full((r, k + 1), -128, dtype=torch.int8, device=DEV)[:, 1:]
+        return _ints((r, k + 1), seed)[:, 1:]
+
+    a, b = rows(m, 1), rows(n, 2)
+    sa, sb = torch.rand(m, device=DEV), torch.rand(n, device=DEV)
+    d = torch.empty((m, n), device=DEV)
+    ouo.int8_matmul(a, sa, b, sb, d)
+    e = _exact_product(a, sa, b, sb)
+    assert np.all(np.abs(to64(d) - e) <= ((1 + U32) ** 4 - 1) * np.abs(e))
+
+
+def test_deep_products_in_a_batch():
+    """Beside products of ordinary depth; each as it is alone."""
+    shapes = [(3, 40, 64), (3, 40, 131072), (300, 300, 256), (20, 500, 152064), (1, 16, 140000)]
+    As = [ouo.int8_empty(m, k).copy_(_ints((m, k), i)) for i, (m, _, k) in enumerate(shapes)]
+    Bs = [ouo.int8_empty(n, k).copy_(_ints((n, k), 9 + i)) for i, (_, n, k) in enumerate(shapes)]
+    sa = [torch.rand(m, device=DEV) for m, _, _ in shapes]
+    sb = [torch.rand(n, device=DEV) for _, n, _ in shapes]
+    Ds = [torch.empty((m, n), device=DEV) for m, n, _ in shapes]
+    ouo.int8_matmul(As, sa, Bs, sb, Ds)
+    for a, x, b, y, d in zip(As, sa, Bs, sb, Ds):
+        one = torch.empty_like(d)
+        ouo.int8_matmul(a, x, b, y, one)
+        e = _exact_product(a, x, b, y)
+        assert torch.equal(one, d)
+        assert np.all(np.abs(to64(d) - e) <= ((1 + U32) ** 4 - 1) * np.abs(e))
+
+
+@pytest.mark.parametrize("vocab", [131072, 152064])
+def test_head_of_a_large_vocabulary(vocab):
+    """An 8-bit head against a teacher, forward and backward: the input
+    gradient's depth is the vocabulary."""
+    tokens, dim, k = 48, 128, 16
+    g = torch.Generator(DEV).manual_seed(7)
+    W = (0.1 * torch.randn((vocab, dim), generator=g, device=DEV)).to(BF)
+    x = torch.randn((tokens, dim), generator=g, device=DEV).to(BF)
+    e = lambda *s, d=F32: torch.empty(s, dtype=d, device=DEV)  # noqa: E731
+    q = lambda r, c: (ouo.int8_empty(r, c), e(r))  # noqa: E731
+    wq, wt, xq, xt, dq, dt = (q(*s) for s in ((vocab, dim), (dim, vocab), (tokens, dim),
+                                              (dim, tokens), (tokens, vocab), (vocab, tokens)))
+    teacher = torch.randn((tokens, k), generator=g, device=DEV)
+    idx = torch.randint(0, vocab, (tokens, k), generator=g, device=DEV).to(torch.int32)
+    S, dS, loss, lse = e(tokens, vocab, d=BF), e(tokens, vocab, d=BF), e(tokens), e(tokens)
+    dx, dW = e(tokens, dim, d=BF), e(vocab, dim)
+    ouo.quantize_int8(W, *wq)
+    ouo.quantize_int8(W, *wt, transpose=True)
+    ouo.quantize_int8(x, *xq)
+    ouo.quantize_int8(x, *xt, transpose=True)
+    ouo.int8_matmul(*xq, *wq, S)
+    ouo.distill_loss(S, teacher, idx, loss, lse)
+    ouo.distill_loss_backward(S, teacher, idx, lse, torch.ones_like(loss), dS)
+    ouo.quantize_int8(dS, *dq)
+    ouo.quantize_int8(dS, *dt, transpose=True)
+    ouo.int8_matmul(*dq, *wt, dx)
+    ouo.int8_matmul(*dt, *xt, dW)
+    bf = (1 + 2.0 ** -8) * (1 + U32) ** 3 - 1
+    for out, (a, sa), (b, sb), tol in ((S, xq, wq, bf), (dx, dq, wt, bf),
+                                       (dW, dt, xt, (1 + U32) ** 4 - 1)):
+        want = _exact_product(a, sa, b, sb)
+        assert np.all(np.abs(to64(out) - want) <= tol * np.abs(want))
+    # 8-bit operands: half a step of each, summed over the vocabulary
+    d, w = to64(dS), to64(W)
+    a, b = np.abs(d).max(1) / 254, np.abs(w).max(0) / 254
+    slack = np.abs(d).sum(1)[:, None] * b + a[:, None] * np.abs(w).sum(0) + vocab * a[:, None] * b
+    want = d @ w
+    assert np.all(np.abs(to64(dx) - want) <= slack * 1.001 + 2.0 ** -8 * np.abs(want))
+    assert torch.isfinite(loss).all() and (loss > 0).all()
