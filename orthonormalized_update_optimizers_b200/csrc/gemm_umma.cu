@@ -198,6 +198,23 @@ __device__ __forceinline__ uint16_t* out_bf16_at(const UmmaArgs& a,
 }
 
 // Output bases of one matrix of a segment (workspace or caller memory).
+// A finished 32 x 32 chunk at (row0, col0) from its staging buffer, by plain
+// stores: of matrix z of a segment whose output is one batch.
+__device__ __noinline__ void store_plain(const Segment& sg, int64_t z, int64_t row0, int64_t col0,
+                                         const float* stg, bool bf16) {
+  const int lane = threadIdx.x & 31;
+  if (col0 + lane >= sg.N) return;
+  const int rows = (int)(sg.M - row0 < 32 ? sg.M - row0 : 32);
+  if (bf16) {
+    const uint16_t* stg16 = reinterpret_cast<const uint16_t*>(stg);
+    uint16_t* o = sg.Ob + z * sg.sob + row0 * sg.ldob + col0 + lane;
+    for (int r = 0; r < rows; ++r) o[r * sg.ldob] = stg16[stg16_idx(r, lane)];
+  } else {
+    float* o = sg.Of + z * sg.sof + row0 * sg.ldof + col0 + lane;
+    for (int r = 0; r < rows; ++r) o[r * sg.ldof] = stg[stg_idx(r, lane)];
+  }
+}
+
 struct TileOut {
   float* f;
   uint16_t* h;
@@ -615,6 +632,11 @@ umma_gemm_kernel(const __grid_constant__ UmmaArgs a) {
         const bool obf = a.has_bf16 != 0;
         const float alpha = a.has_dalpha ? a.dalpha[sg.dbase + b] : a.alpha;
         bool ok_c0 = true;
+        // The TMA store clips a box at 16 bytes, not at the element: over the
+        // last column of rows that end elsewhere it would write zeros to what
+        // follows them (a wider matrix's other columns).
+        const int ip_plain =
+            (sg.N & (obf ? 7 : 3)) != 0 && tj * BN + ip_half * (BN / 2) + nch * 32 > sg.N ? nch - 1 : -1;
 #pragma unroll 1
         for (int c = 0; c < nch; ++c) {
           const uint32_t sb = (ip_base + (uint32_t)c) & (C::kStg - 1);
@@ -661,6 +683,14 @@ umma_gemm_kernel(const __grid_constant__ UmmaArgs a) {
               }
               *pp = make_uint4(ow[0], ow[1], ow[2], ow[3]);
             }
+          }
+          if (c == ip_plain) {  // the warp's last chunk
+            __syncwarp();
+            store_plain(sg, ip_z, ip_row, gj0, stg, obf);
+            ptx::fence_async_shared();  // the buffer's next load is the TMA's
+            __syncwarp();
+            ++nstores;
+            break;
           }
           ptx::fence_async_shared();
           __syncwarp();
