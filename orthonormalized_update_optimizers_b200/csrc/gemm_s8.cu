@@ -339,7 +339,7 @@ s8_pair_kernel(const __grid_constant__ S8Args a) {
       report_status(a.status, OUO_STATUS_TIMEOUT);
     }
     ptx::mma2_commit(drain, 0x1);
-    ptx::mbar_wait_timed(drain, 0, kWaitLimitNs);
+    if (!ptx::mbar_wait_timed(drain, 0, kWaitLimitNs)) report_status(a.status, OUO_STATUS_TIMEOUT);
   } else if (warp >= 2) {
     // epilogue: one TMEM lane quarter and half of the columns per warp
     const uint32_t q = (uint32_t)(warp & 3), half = (uint32_t)((warp - 2) >> 2);
@@ -583,7 +583,7 @@ s8_split_kernel(const __grid_constant__ SplitArgs a) {
     }
     ptx::mma_commit(done);
     // after an aborted loop too: TMEM is released only when this is over
-    ptx::mbar_wait_timed(done, 0, kWaitLimitNs);
+    if (!ptx::mbar_wait_timed(done, 0, kWaitLimitNs)) report_status(a.status, OUO_STATUS_TIMEOUT);
   }
   __syncwarp();
   // The products are done and the stages free, in every CTA of the cluster.

@@ -557,7 +557,7 @@ umma_gemm_kernel(const __grid_constant__ UmmaArgs a) {
     // is released
     if (CG == 2) ptx::mma2_commit(drain, 0x1);
     else ptx::mma_commit(drain);
-    ptx::mbar_wait_timed(drain, 0, kWaitLimitNs);
+    if (!ptx::mbar_wait_timed(drain, 0, kWaitLimitNs)) report_status(a.status, OUO_STATUS_TIMEOUT);
   } else if (warp >= 2) {
     // ------------------------------------------------------------- epilogue
     const uint32_t q = (uint32_t)(warp & 3);  // TMEM lanes 32q .. 32q+31
