@@ -430,6 +430,10 @@ int dion_shard_update(const ouo_mat* M, const ouo_mat* Q_state,
  * need them in A and B).
  * Sums, norms and softmax statistics are held in fp32 or wider.
  * 8-bit matrices hold signed integers, one byte each (`ld` in bytes).
+ * An output must be apart from the inputs and the other outputs, unless a call
+ * says that it may be an input itself (same pointer, type and pitch).  Overlap
+ * is refused, also between columns of one wider matrix; not seen is only that of
+ * two matrices with gaps between their rows and different pitches.
  */
 
 /*
@@ -444,7 +448,7 @@ int dion_shard_update(const ouo_mat* M, const ouo_mat* Q_state,
  * an infinity gets scale NaN and zeros, so that every product with it is
  * NaN.  scale: host array of nmat device pointers.  X: dtype x_dtype.
  * Large transposed matrices need a workspace (16-byte aligned; 0 bytes
- * otherwise).  Q and X must not overlap.  Use:
+ * otherwise).  Use:
  * the weights after apply_update (both orders: products with W and with its
  * transpose), activations, gradients.
  */
@@ -460,8 +464,7 @@ int quantize_int8(const ouo_mat* X, int x_dtype, const ouo_mat* Q,
  * exact in 32 bits, then (sum * a_scale) * b_scale in fp32, rounded once to
  * D's type.  D[i]: M x N, dtype d_dtype.  a_scale, b_scale: host arrays of
  * nmat device pointers, M and N floats.  K <= OUO_INT8_MAX_DEPTH; K = 0
- * writes zeros times the scales.  M and N may be 0.  D must not overlap the
- * operands.  With operands from quantize_int8 the three products of a linear
+ * writes zeros times the scales.  M and N may be 0.  With operands from quantize_int8 the three products of a linear
  * layer Y = X W^T are
  *   Y  = int8_matmul(q(X), q(W)),  dX = int8_matmul(q(dY), q^T(W)),
  *   dW = int8_matmul(q^T(dY), q^T(X)),   q^T = quantize_int8 transposed,
@@ -488,8 +491,7 @@ int int8_matmul_deep(const ouo_mat* A, const float* const* a_scale,
  * Outputs, at least one of Y and Q: Y (y rounded to y_dtype); Q and scale (y
  * in 8 bits as quantize_int8 without transposition); rstd (optional, r per
  * row, for the gradient).  residual and H share h_dtype; H may be the residual
- * or X itself (same pointer, type and pitch).  Other outputs must not overlap
- * inputs.  weight: device vector of cols elements, w_dtype.  The squares are
+ * or X itself, and Y may be X itself when Q is NULL.  weight: device vector of cols elements, w_dtype.  The squares are
  * summed in fp32: |h| is expected below 1e16 or so.
  *
  * rms_norm_backward -- dY: gradient of y (through the 8-bit rounding it
@@ -534,7 +536,7 @@ int rms_norm_backward(const ouo_mat* dY, int dy_dtype, const ouo_mat* H,
  * float[rows]), lse from distill_loss:
  *   dS_tv = dloss_t tau (q_v - sum_{k: idx_k = v} p_k)
  * Rows with dloss 0 or without entries get zeros, whatever S holds there.
- * dS may be S itself (same type and pitch), else they must not overlap.
+ * dS may be S itself.
  */
 int distill_loss(const ouo_mat* S, int s_dtype, const ouo_mat* teacher,
                  int t_dtype, const ouo_mat* idx, float temperature,

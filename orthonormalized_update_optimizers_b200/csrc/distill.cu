@@ -515,6 +515,10 @@ int distill_loss(const ouo_mat* S, int s_dtype, const ouo_mat* teacher, int t_dt
   OUO_TRY(validate_vec(lse, S->rows, 4, "lse"));
   if (S->rows == 0) return OUO_OK;
   OUO_TRY(require_sm100());
+  OUO_TRY(validate_apart({operand(loss, S->rows, 4, "loss"), operand(lse, S->rows, 4, "lse")},
+                         {operand(*S, (int64_t)elem_size(s_dtype), "S"),
+                          operand(*teacher, (int64_t)elem_size(t_dtype), "teacher"),
+                          operand(*idx, 4, "idx")}));
   DistillArgs a = distill_args(S, s_dtype, teacher, t_dtype, idx, temperature);
   a.loss = loss;
   a.lse = lse;
@@ -562,6 +566,11 @@ int distill_loss_backward(const ouo_mat* S, int s_dtype, const ouo_mat* teacher,
   OUO_TRY(validate_vec(dloss, S->rows, 4, "dloss"));
   if (S->rows == 0) return OUO_OK;
   OUO_TRY(require_sm100());
+  OUO_TRY(validate_apart({operand(*dS, (int64_t)elem_size(ds_dtype), "dS", S->ptr)},
+                         {operand(*S, (int64_t)elem_size(s_dtype), "S"),
+                          operand(*teacher, (int64_t)elem_size(t_dtype), "teacher"),
+                          operand(*idx, 4, "idx"), operand(lse, S->rows, 4, "lse"),
+                          operand(dloss, S->rows, 4, "dloss")}));
   DistillArgs a = distill_args(S, s_dtype, teacher, t_dtype, idx, temperature);
   a.lse = const_cast<float*>(lse);
   a.dloss = dloss;

@@ -953,6 +953,11 @@ int matmul(int64_t deepest, const ouo_mat* A, const float* const* a_scale, const
     OUO_TRY(validate_vec(b_scale[i], B[i].rows, 4, "b_scale"));
   }
   OUO_TRY(require_sm100());
+  for (int i = 0; i < nmat; ++i)
+    OUO_TRY(validate_apart({operand(D[i], (int64_t)elem_size(d_dtype), "D")},
+                           {operand(A[i], 1, "A"), operand(B[i], 1, "B"),
+                            operand(a_scale[i], A[i].rows, 4, "a_scale"),
+                            operand(b_scale[i], B[i].rows, 4, "b_scale")}));
   cudaStream_t s = (cudaStream_t)stream;
   for (int i = 0; i < nmat; ++i) {
     OUO_TRY(product(Product{A[i], B[i], D[i], a_scale[i], b_scale[i], d_dtype == OUO_BF16,

@@ -470,8 +470,21 @@ int rms_norm(const ouo_mat* X, int x_dtype, const ouo_mat* residual, const ouo_m
   }
   OUO_TRY(validate_vec(weight, n, elem_size(w_dtype), "weight"));
   OUO_TRY(validate_vec(rstd, 0, 4, "rstd"));
+  if (Y && !Q) OUO_TRY(validate_in_place(*Y, y_dtype, *X, x_dtype, "Y and X"));
   if (T == 0) return OUO_OK;
   OUO_TRY(require_sm100());
+  {
+    const ouo_mat none{};
+    const int64_t hs = residual || H ? (int64_t)elem_size(h_dtype) : 1;
+    OUO_TRY(validate_apart(
+        {operand(H ? *H : none, hs, "H", X->ptr, residual ? residual->ptr : nullptr),
+         operand(Y ? *Y : none, Y ? (int64_t)elem_size(y_dtype) : 1, "Y", Q ? nullptr : X->ptr),
+         operand(Q ? *Q : none, 1, "Q"), operand(Q ? scale : nullptr, T, 4, "scale"),
+         operand(rstd, T, 4, "rstd")},
+        {operand(*X, (int64_t)elem_size(x_dtype), "X"),
+         operand(residual ? *residual : none, hs, "residual"),
+         operand(weight, n, (int64_t)elem_size(w_dtype), "weight")}));
+  }
   NormArgs a{};
   a.X = X->ptr; a.ldx = X->ld; a.x_bf16 = x_dtype == OUO_BF16;
   if (residual) { a.R = residual->ptr; a.ldr = residual->ld; }
@@ -549,6 +562,15 @@ int rms_norm_backward(const ouo_mat* dY, int dy_dtype, const ouo_mat* H, int h_d
     return set_error(OUO_ERR_WORKSPACE, "workspace: %zu bytes needed (16-byte aligned), %zu given",
                      need, ws ? ws_bytes : (size_t)0);
   OUO_TRY(require_sm100());
+  {
+    const ouo_mat none{};
+    const int64_t xs = (int64_t)elem_size(dx_dtype);
+    OUO_TRY(validate_apart(
+        {operand(*dX, xs, "dX", dY->ptr, dH ? dH->ptr : nullptr), operand(dweight, n, 4, "dweight")},
+        {operand(*dY, (int64_t)elem_size(dy_dtype), "dY"),
+         operand(*H, (int64_t)elem_size(h_dtype), "H"), operand(dH ? *dH : none, xs, "dH"),
+         operand(weight, n, (int64_t)elem_size(w_dtype), "weight"), operand(rstd, T, 4, "rstd")}));
+  }
   cudaStream_t s = (cudaStream_t)stream;
   const int64_t parts = bwd_parts(T, n);
   if (T > 0) {

@@ -610,6 +610,9 @@ extern "C" int quantize_int8(const ouo_mat* X, int x_dtype, const ouo_mat* Q, fl
     return set_error(OUO_ERR_WORKSPACE, "workspace: %zu bytes needed (16-byte aligned), %zu given",
                      need, ws ? ws_bytes : (size_t)0);
   OUO_TRY(require_sm100());
+  for (int i = 0; i < nmat; ++i)
+    OUO_TRY(validate_apart({operand(Q[i], 1, "Q"), operand(scale[i], Q[i].rows, 4, "scale")},
+                           {operand(X[i], (int64_t)elem_size(x_dtype), "X")}));
   cudaStream_t s = (cudaStream_t)stream;
   const int bf16 = x_dtype == OUO_BF16;
   if (transpose) {

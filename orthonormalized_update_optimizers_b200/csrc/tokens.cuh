@@ -4,10 +4,12 @@
 // rounding to 8 bits.
 #pragma once
 
+#include <initializer_list>
 #include <mutex>
 #include <type_traits>
 
 #include "internal.h"
+#include "overlap.h"
 
 namespace ouo {
 
@@ -52,6 +54,39 @@ inline int validate_vec(const void* p, int64_t n, size_t es, const char* name) {
   if (n > 0 && !p) return set_error(OUO_ERR_INVALID_ARG, "%s: NULL pointer", name);
   if ((uintptr_t)p % es != 0)
     return set_error(OUO_ERR_INVALID_ARG, "%s: not aligned to its element size", name);
+  return OUO_OK;
+}
+
+// What a call reads or writes, for the check that outputs are apart from
+// everything else.  `in_place`: the input that this output may be, if it starts
+// where that does (validate_in_place has looked at the rest).
+struct Operand {
+  Span span;
+  const char* name;
+  const void* in_place = nullptr;
+  const void* in_place2 = nullptr;
+};
+
+inline Operand operand(const ouo_mat& m, int64_t es, const char* name,
+                       const void* in_place = nullptr, const void* in_place2 = nullptr) {
+  return Operand{Span{(uintptr_t)m.ptr, m.rows, m.cols * es, m.ld * es}, name, in_place, in_place2};
+}
+inline Operand operand(const void* p, int64_t n, int64_t es, const char* name) {
+  return Operand{Span{(uintptr_t)p, p ? 1 : 0, n * es, n * es}, name};
+}
+
+inline int validate_apart(std::initializer_list<Operand> outs, std::initializer_list<Operand> ins) {
+  for (const Operand* o = outs.begin(); o != outs.end(); ++o) {
+    for (const Operand& i : ins) {
+      const void* p = (const void*)i.span.p;
+      if (p == (const void*)o->span.p && p && (p == o->in_place || p == o->in_place2)) continue;
+      if (overlap(o->span, i.span))
+        return set_error(OUO_ERR_INVALID_ARG, "%s and %s overlap", o->name, i.name);
+    }
+    for (const Operand* q = o + 1; q != outs.end(); ++q)
+      if (overlap(o->span, q->span))
+        return set_error(OUO_ERR_INVALID_ARG, "%s and %s overlap", o->name, q->name);
+  }
   return OUO_OK;
 }
 

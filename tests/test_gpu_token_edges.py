@@ -6,6 +6,7 @@ import torch
 
 import orthonormalized_update_optimizers_b200 as ouo
 from oracle import tokens as ot
+from orthonormalized_update_optimizers_b200._lib import OuoError
 
 from ._util import to64
 
@@ -87,6 +88,74 @@ def test_rms_norm_rounds_ties_to_even(cols, dtype):
         w = torch.tensor(np.resize(x[a], cols), device=DEV).to(dtype)
         ouo.rms_norm(h, w, Q=got, scale=scale, eps=0.0)
         assert np.array_equal(to64(got), sign * np.resize(q[a], cols))
+
+
+# ------------------------------------------------------ outputs over inputs
+
+
+def test_outputs_over_inputs_are_refused():
+    """By the host, before a launch: every buffer is as it was."""
+    x = torch.randn((40, 64), device=DEV)
+    w = torch.ones(64, device=DEV)
+    r, h, y = torch.randn_like(x), torch.empty_like(x), torch.empty_like(x)
+    v = torch.empty(40, device=DEV)
+    i8 = x.view(torch.int8)  # 40 x 256
+    q = ouo.int8_empty(40, 64)
+    t, idx = torch.randn((40, 4), device=DEV), torch.zeros((40, 4), dtype=torch.int32, device=DEV)
+    a, b = torch.zeros((40, 64), dtype=torch.int8, device=DEV), ouo.int8_empty(16, 64).zero_()
+    wide = torch.randn((40, 128), device=DEV)
+    keep = [k.clone() for k in (x, w, r, t, a, wide)]
+    rms, bwd, kd, kdb = ouo.rms_norm, ouo.rms_norm_backward, ouo.distill_loss, ouo.distill_loss_backward
+    calls = [
+        ("Q and X", lambda: ouo.quantize_int8(x, i8[:, :64], v)),
+        ("scale and X", lambda: ouo.quantize_int8(x, q, x[0])),
+        ("D and A", lambda: ouo.int8_matmul(a, v, b, w, a.view(torch.float32)[:, :16])),
+        ("D and b_scale", lambda: ouo.int8_matmul(a[:1], v, b, w, w[None, 8:24])),
+        ("Y and X", lambda: rms(x, w, Y=x, Q=q, scale=v)),
+        ("Y and residual", lambda: rms(x, w, Y=r, residual=r, H=h)),
+        ("H and Y", lambda: rms(x, w, Y=r, residual=r, H=r)),
+        ("H and X", lambda: rms(x[1:], w, Y=y[1:], H=x[:39])),
+        ("Q and X", lambda: rms(x, w, Q=i8[:, :64], scale=v)),
+        ("rstd and weight", lambda: rms(x, w, Y=y, rstd=w)),
+        ("scale and rstd", lambda: rms(x, w, Q=q, scale=v, rstd=v)),
+        ("Y and X", lambda: rms(wide[:, :64], w, Y=wide[:, 32:96])),
+        ("dX and H", lambda: bwd(x, r, w, v, r)),
+        ("dX and dY", lambda: bwd(x[1:], r[1:], w, v, x[:39])),
+        ("dX and dH", lambda: bwd(y[1:], r[1:], w, v, x[:39], dH=x[1:])),
+        ("dweight and weight", lambda: bwd(x, r, w, v, y, dweight=w)),
+        ("dX and dweight", lambda: bwd(x, r, w, v, y, dweight=y[1])),
+        ("loss and S", lambda: kd(x, t, idx, x[0], v)),
+        ("loss and lse", lambda: kd(x, t, idx, v, v)),
+        ("dS and S", lambda: kdb(x[1:], t[1:], idx[1:], v, v, x[:39])),
+        ("dS and teacher", lambda: kdb(x[:, :4], t, idx, v, v, t)),
+    ]
+    for what, call in calls:
+        with pytest.raises(OuoError, match=what + " overlap"):
+            call()
+    torch.cuda.synchronize()
+    assert all(torch.equal(k, m) for k, m in zip(keep, (x, w, r, t, a, wide)))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("cols", [64, 1000, 4097, 20001])
+def test_rms_norm_in_place(cols, dtype):
+    x = torch.randn((9, cols), device=DEV).to(dtype)
+    w = torch.rand(cols, device=DEV).to(dtype)
+    y, r1, r2 = torch.empty_like(x), torch.empty(9, device=DEV), torch.empty(9, device=DEV)
+    ouo.rms_norm(x, w, Y=y, rstd=r1)
+    ouo.rms_norm(x, w, Y=x, rstd=r2)
+    assert torch.equal(x, y) and torch.equal(r1, r2)
+
+
+def test_columns_of_one_buffer():
+    """Inputs and outputs that are columns of one wider matrix are apart."""
+    buf = torch.randn((33, 3 * 128), device=DEV)
+    x, y, h = buf[:, :128], buf[:, 128:256], buf[:, 256:]
+    w, keep = torch.rand(128, device=DEV), x.clone()
+    want = torch.empty_like(keep)
+    ouo.rms_norm(keep, w, Y=want)
+    ouo.rms_norm(x, w, Y=y, H=h)
+    assert torch.equal(x, keep) and torch.equal(y, want) and torch.equal(h, keep)
 
 
 # ------------------------------------------------------ workspaces and streams
