@@ -570,6 +570,40 @@ int quant_cols2(const ouo_mat& X, const ouo_mat& Q, float* scale, void* ws, cuda
   return OUO_OK;
 }
 
+// The kinds of a batch's matrices, each with launches of its own, so that one
+// that cannot take 16-byte accesses, or whose rows do not fit in registers,
+// does not slow the others down.
+enum { kRowsVec, kRowsElem, kRowsLong };
+
+int rows_kind(const ouo_mat& x, size_t es) {
+  if (x.cols == 0) return kRowsVec;
+  if (x.cols > kTeamMost) return kRowsLong;
+  return rows16(x, es) && x.cols % 8 == 0 ? kRowsVec : kRowsElem;
+}
+
+// One launch; the longest rows choose its teams.
+int quant_rows(QuantArgs& a, int64_t rows, int64_t longest, int kind, cudaStream_t s) {
+  if (rows == 0) return OUO_OK;
+  a.row_start[a.nmat] = rows;
+  if (kind == kRowsLong) {
+    quant_long_kernel<<<(unsigned)rows, 512, 0, s>>>(a);
+    OUO_CHECK_LAUNCH();
+    return OUO_OK;
+  }
+  // (element by element too, a quantized row is one load and one store: the
+  // smaller teams of the vector modes do better)
+  const Team t = team_for(rows, longest, a.bf16 ? 1 : 2);
+  const int mode = (a.bf16 ? 1 : 2) + (kind == kRowsElem ? 2 : 0);
+  return with_team(t, mode, [&](auto tpr, auto nv, auto md) -> int {
+    constexpr int TPR = decltype(tpr)::value, NV = decltype(nv)::value;
+    constexpr int MODE = decltype(md)::value;
+    constexpr int kTeams = kTeamThreads<TPR> / TPR;
+    quant_rows_kernel<TPR, NV, MODE><<<(unsigned)ceil_div(rows, (int64_t)kTeams), kTeamThreads<TPR>, 0, s>>>(a);
+    OUO_CHECK_LAUNCH();
+    return OUO_OK;
+  });
+}
+
 }  // namespace
 }  // namespace ouo
 
@@ -627,49 +661,33 @@ extern "C" int quantize_int8(const ouo_mat* X, int x_dtype, const ouo_mat* Q, fl
     }
     return OUO_OK;
   }
-  // One launch per kChunk matrices; the longest rows choose its teams.
-  for (int c0 = 0; c0 < nmat; c0 += kChunk) {
-    const int cn = nmat - c0 < kChunk ? nmat - c0 : kChunk;
+  for (int kind = 0; kind < 3; ++kind) {
     QuantArgs a;
-    a.nmat = cn;
     a.bf16 = bf16;
-    int64_t acc = 0, longest = 0;
-    for (int i = 0; i < cn; ++i) {
-      const ouo_mat& x = X[c0 + i];
-      a.row_start[i] = acc;
-      a.cols[i] = x.cols;
-      a.X[i] = x.ptr;
-      a.ldx[i] = x.ld;
-      a.Q[i] = (int8_t*)Q[c0 + i].ptr;
-      a.ldq[i] = Q[c0 + i].ld;
-      a.scale[i] = scale[c0 + i];
-      a.vecx[i] = rows16(x, elem_size(x_dtype));
-      a.vecq[i] = (uintptr_t)a.Q[i] % 8 == 0 && (x.rows <= 1 || a.ldq[i] % 8 == 0);
-      acc += x.rows;
-      if (x.rows > 0 && x.cols > longest) longest = x.cols;
+    a.nmat = 0;
+    int64_t rows = 0, longest = 0;
+    for (int i = 0; i < nmat; ++i) {
+      const ouo_mat &x = X[i], &q = Q[i];
+      if (x.rows == 0 || rows_kind(x, elem_size(x_dtype)) != kind) continue;
+      if (a.nmat == kChunk || rows + x.rows > 0x7fffffff) {
+        OUO_TRY(quant_rows(a, rows, longest, kind, s));
+        a.nmat = 0;
+        rows = longest = 0;
+      }
+      const int g = a.nmat++;
+      a.row_start[g] = rows;
+      a.cols[g] = x.cols;
+      a.X[g] = x.ptr;
+      a.ldx[g] = x.ld;
+      a.Q[g] = (int8_t*)q.ptr;
+      a.ldq[g] = q.ld;
+      a.scale[g] = scale[i];
+      a.vecx[g] = rows16(x, elem_size(x_dtype));
+      a.vecq[g] = (uintptr_t)q.ptr % 8 == 0 && (x.rows <= 1 || q.ld % 8 == 0);
+      rows += x.rows;
+      if (x.cols > longest) longest = x.cols;
     }
-    a.row_start[cn] = acc;
-    if (acc == 0) continue;
-    if (acc > 0x7fffffff) return set_error(OUO_ERR_UNSUPPORTED, "X: too many rows in one batch");
-    int mode = bf16 ? 1 : 2;
-    for (int i = 0; i < cn; ++i)
-      if (!a.vecx[i] || a.cols[i] % 8 != 0) mode = bf16 ? 3 : 4;
-    // (element by element too, a quantized row is one load and one store: the
-    // smaller teams of the vector modes do better)
-    const Team t = team_for(acc, longest, bf16 ? 1 : 2);
-    if (t.tpr == 0) {
-      quant_long_kernel<<<(unsigned)acc, 512, 0, s>>>(a);
-      OUO_CHECK_LAUNCH();
-      continue;
-    }
-    OUO_TRY(with_team(t, mode, [&](auto tpr, auto nv, auto md) -> int {
-      constexpr int TPR = decltype(tpr)::value, NV = decltype(nv)::value;
-      constexpr int MODE = decltype(md)::value;
-      constexpr int kTeams = kTeamThreads<TPR> / TPR;
-      quant_rows_kernel<TPR, NV, MODE><<<(unsigned)ceil_div(acc, (int64_t)kTeams), kTeamThreads<TPR>, 0, s>>>(a);
-      OUO_CHECK_LAUNCH();
-      return OUO_OK;
-    }));
+    OUO_TRY(quant_rows(a, rows, longest, kind, s));
   }
   return OUO_OK;
 }

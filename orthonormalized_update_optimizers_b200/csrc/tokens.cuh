@@ -344,12 +344,14 @@ __device__ __forceinline__ void store_row(void* p, int t, int n, int bf16, int v
   }
 }
 
+constexpr int64_t kTeamMost = 512 * 4 * 8;  // elements that a block's registers take
+
 // How a matrix of rows x cols is given to teams: enough threads per row that
 // a thread holds at most 8 chunks, and whole blocks per row where there are
 // too few rows to fill the GPU with warps (a row's latency counts then), or
 // where a row is read element by element (modes 3 and 4: then every element
 // costs registers, and fewer a thread leave more threads to wait with).
-// cols above 16384 do not fit: TPR 0.
+// cols above kTeamMost do not fit: TPR 0.
 struct Team {
   int tpr, nv;
 };
@@ -357,7 +359,7 @@ struct Team {
 inline Team team_for(int64_t rows, int64_t cols, int mode) {
   const int64_t chunks = ceil_div(cols, (int64_t)8);
   int tpr = chunks <= 32 * 8 ? 32 : chunks <= 128 * 8 ? 128 : 512;
-  if (chunks > 512 * 4) return Team{0, 0};
+  if (cols > kTeamMost) return Team{0, 0};
   if (rows < 4 * num_sms() || mode == 3 || mode == 4) tpr = chunks <= 128 ? (chunks <= 32 ? 32 : 128) : 512;
   int nv = 1;
   while ((int64_t)tpr * nv < chunks) nv *= 2;

@@ -192,6 +192,32 @@ def test_workspace_of_another_stream_is_not_one_that_is_still_in_use():
         torch.cuda.synchronize()
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_quantize_batch_of_all_kinds(dtype):
+    """Aligned, odd, long and empty matrices in one call: each as alone, and
+    each kind in a launch of its own."""
+    g = torch.Generator(DEV).manual_seed(1)
+    shapes = [(70, 256), (3, 20000), (9, 129), (0, 7), (4, 0), (300, 1024), (2, 16385), (5, 16384),
+              (1, 1), (33, 8)]
+    xs = [torch.randn(s, generator=g, device=DEV).to(dtype) for s in shapes]
+    xs.append(torch.randn((8, 65), generator=g, device=DEV).to(dtype)[:, 1:])  # odd pitch, 64 wide
+    qs = [ouo.int8_empty(*x.shape).fill_(7) for x in xs]
+    ss = [torch.full((x.shape[0] + 1,), 77.0, device=DEV) for x in xs]
+
+    def launches(*args):
+        before = ouo.launch_count()
+        ouo.quantize_int8(*args)
+        return ouo.launch_count() - before
+
+    assert launches(xs, qs, ss) == 3
+    for x, q, s in zip(xs, qs, ss):
+        one, so = ouo.int8_empty(*x.shape), torch.full((x.shape[0] + 1,), 77.0, device=DEV)
+        assert launches(x, one, so) == (x.shape[0] > 0)
+        assert torch.equal(q, one) and torch.equal(s, so)
+    # an empty matrix has no say, whatever its length
+    assert launches([xs[0], xs[3]], [qs[0], qs[3]], [ss[0], ss[3]]) == 1
+
+
 # ------------------------------------------- temperatures far from the usual
 
 
