@@ -448,3 +448,39 @@ def test_head_of_a_large_vocabulary(vocab):
     want = d @ w
     assert np.all(np.abs(to64(dx) - want) <= slack * 1.001 + 2.0 ** -8 * np.abs(want))
     assert torch.isfinite(loss).all() and (loss > 0).all()
+
+
+# ------------------------------------------- the gradient, value by value
+
+
+@pytest.mark.parametrize("dtype,out", [(BF, BF), (F32, F32), (BF, F32), (F32, BF)])
+@pytest.mark.parametrize("tau", [1.0, 2.0, 0.7])
+@pytest.mark.parametrize("rows,vocab,k", [
+    (1, 50001, 20), (33, 4099, 64), (70, 2048, 7), (2, 131072, 128), (9, 32768, 1024),
+    (300, 515, 33), (700, 64, 5), (1300, 20000, 16)])
+def test_distill_gradient_value_by_value(rows, vocab, k, tau, dtype, out):
+    g = torch.Generator(DEV).manual_seed(vocab)
+    s = (torch.randn((rows, vocab), generator=g, device=DEV) * 3).to(dtype)
+    t = torch.randn((rows, k), generator=g, device=DEV) * 2 + 5
+    idx = torch.randint(0, vocab, (rows, k), generator=g, device=DEV).to(torch.int32)
+    loss, lse = torch.empty(rows, device=DEV), torch.empty(rows, device=DEV)
+    ouo.distill_loss(s, t, idx, loss, lse, temperature=tau)
+    dl = torch.randn(rows, generator=g, device=DEV)
+    ds = torch.empty((rows, vocab), dtype=out, device=DEV)
+    ouo.distill_loss_backward(s, t, idx, lse, dl, ds, temperature=tau)
+    # in float64 on the device: the oracle's sums one by one would take minutes
+    x = s.double() / tau
+    q = torch.exp(x - lse.double()[:, None])
+    lp = torch.log_softmax(t.double() / tau, 1)
+    p = torch.zeros_like(q).scatter_add_(1, idx.long(), lp.exp())
+    scale = (dl.double() * tau)[:, None]
+    e = scale * (q - p)
+    z = (x.abs().max() + lse.abs().max()).item()
+    zt = (t.abs().max() / tau).item()
+    # q's exponent: 1 / tau, the fused product, log2(e) (2); the exponential (2
+    # ulp); g and its product.  p's: two in the difference by tau, 1 / tau; the
+    # exponential, its sum and quotient, equal indices
+    eq = (4 * z + 8) * U32 * q
+    ep = (6 * zt + k / 128 + 52) * U32 * p
+    tol = scale.abs() * (eq + ep + 2.0 ** -126) + ({BF: 2.0 ** -8, F32: U32}[out] + U32) * e.abs()
+    assert bool(((ds.double() - e).abs() <= tol).all())
