@@ -699,25 +699,6 @@ s8_split_kernel(const __grid_constant__ SplitArgs a) {
 
 // ------------------------------------------------------------------- host
 
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-  static EncodeTiledFn fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                         &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(p);
-  });
-  return fn;
-}
-
 int make_map(CUtensorMap* map, const ouo_mat& m, CUtensorMapDataType type, size_t es,
              uint32_t box_cols, uint32_t box_rows, CUtensorMapSwizzle swz) {
   EncodeTiledFn fn = encode_fn();
@@ -892,12 +873,12 @@ int product(const Product& p, cudaStream_t s) {
   const int64_t M = p.D.rows, N = p.D.cols, K = p.A.cols;
   if (M == 0 || N == 0) return OUO_OK;
   if (K == 0 || !rows16(p.A, 1) || !rows16(p.B, 1)) return run_simt(p, s);
-  // One or two tokens: 11.4 / 13.4 us at 14336 x 4096 against 14.9 in the split
-  // kernel; four are its (21.0 against 15.0).
+  // One or two tokens: 10.9 / 12.2 us at 14336 x 4096 against 13.9 / 14.1 in the
+  // split kernel.
   if (M == 1) return run_vec<1>(p, s);
   if (M == 2) return run_vec<2>(p, s);
-  // Pair tiles once they occupy two thirds of the SMs: 17.6 us at 1024 x 4096 x
-  // 4096 (64 tiles) against 20.5 in the split kernel, 17.1 against 15.8 at half
+  // Pair tiles once they occupy two thirds of the SMs: 18.1 us at 1024 x 4096 x
+  // 4096 (64 tiles) against 20.1 in the split kernel, 17.1 against 15.8 at half
   // the rows (32 tiles).
   const int64_t sms = num_sms();
   if (K <= OUO_INT8_MAX_DEPTH && M > 128 && N > 128 && 3 * ceil_div(M, 256) * ceil_div(N, 256) >= sms) return run_pair(p, s);
@@ -906,9 +887,9 @@ int product(const Product& p, cudaStream_t s) {
   const int64_t T = t_rows ? M : N, R = t_rows ? N : M;
   const int bn = T <= 16 ? 16 : T <= 32 ? 32 : T <= 64 ? 64 : 128;
   // K is divided while the CTAs fit one to an SM and keep enough of it: the
-  // join grows with the tile (128 x 4096 x 4096, 32 tiles: 18.3 / 13.3 / 11.6 /
-  // 15.9 us in 1 / 2 / 4 / 8; 1 x 1024 x 4096, 8 tiles: 12.3 / 7.9 / 5.8 / 4.9).  In
-  // two as long as both halves fit two to an SM (512 x 4096 x 4096: 18.3 / 15.8).
+  // join grows with the tile (128 x 4096 x 4096, 32 tiles: 18.0 / 12.8 / 10.9 /
+  // 14.8 us in 1 / 2 / 4 / 8; 4 x 1024 x 4096, 8 tiles: 12.5 / 8.1 / 5.9 / 4.9).  In
+  // two as long as both halves fit two to an SM (512 x 4096 x 4096: 18.2 / 15.4 / 24.5).
   const int64_t st = ceil_div(R, 128) * ceil_div(T, bn), nk = ceil_div(K, (int64_t)kRowB);
   const int64_t least = bn <= 32 ? 2 : 8;
   int split = 1;

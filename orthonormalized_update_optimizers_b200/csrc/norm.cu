@@ -406,13 +406,19 @@ int launch_bwd_as(const NormBwdArgs& a, unsigned grid, cudaStream_t s) {
   return OUO_OK;
 }
 
+// All matrices in 16-byte accesses; and not all.
 template <int TPR, int NV>
-int launch_bwd(const NormBwdArgs& a, unsigned grid, cudaStream_t s) {
-  const bool vec = a.vdy && a.vh && a.vdx && (a.vdh || !a.dH) && a.cols % 8 == 0;
+int launch_bwd_vec(const NormBwdArgs& a, unsigned grid, cudaStream_t s) {
   const int bf = a.dy_bf16 + a.h_bf16 + a.dx_bf16;
-  if (vec && bf == 1 && a.dy_bf16) return launch_bwd_as<TPR, NV, 5, 2>(a, grid, s);
-  if (vec && bf == 3) return launch_bwd_as<TPR, NV, 1, 4>(a, grid, s);
-  if (vec && bf == 0) return launch_bwd_as<TPR, NV, 2, 2>(a, grid, s);
+  if (bf == 1 && a.dy_bf16) return launch_bwd_as<TPR, NV, 5, 2>(a, grid, s);
+  if (bf == 3) return launch_bwd_as<TPR, NV, 1, 4>(a, grid, s);
+  if (bf == 0) return launch_bwd_as<TPR, NV, 2, 2>(a, grid, s);
+  return launch_bwd_as<TPR, NV, 0, 1>(a, grid, s);
+}
+
+template <int TPR, int NV>
+int launch_bwd_elem(const NormBwdArgs& a, unsigned grid, cudaStream_t s) {
+  const int bf = a.dy_bf16 + a.h_bf16 + a.dx_bf16;
   if (bf == 3) return launch_bwd_as<TPR, NV, 3, 1>(a, grid, s);
   if (bf == 0) return launch_bwd_as<TPR, NV, 4, 1>(a, grid, s);
   return launch_bwd_as<TPR, NV, 0, 1>(a, grid, s);
@@ -591,11 +597,13 @@ int rms_norm_backward(const ouo_mat* dY, int dy_dtype, const ouo_mat* H, int h_d
     a.vdx = rows16(*dX, elem_size(dx_dtype));
     const unsigned grid = (unsigned)parts;
     const bool vec = a.vdy && a.vh && a.vdx && (a.vdh || !dH) && n % 8 == 0;
-    if (n <= 128 * 8) OUO_TRY((launch_bwd<128, 1>(a, grid, s)));
-    else if (n <= 512 * 8 && !vec) OUO_TRY((launch_bwd<512, 1>(a, grid, s)));
-    else if (n <= 128 * 16) OUO_TRY((launch_bwd<128, 2>(a, grid, s)));
-    else if (n <= 256 * 16) OUO_TRY((launch_bwd<256, 2>(a, grid, s)));
-    else if (n <= 512 * 16) OUO_TRY((launch_bwd<512, 2>(a, grid, s)));
+    if (n <= 128 * 8)
+      OUO_TRY((vec ? launch_bwd_vec<128, 1> : launch_bwd_elem<128, 1>)(a, grid, s));
+    else if (n <= 512 * 8 && !vec) OUO_TRY((launch_bwd_elem<512, 1>(a, grid, s)));
+    else if (n <= 128 * 16) OUO_TRY((launch_bwd_vec<128, 2>(a, grid, s)));
+    else if (n <= 256 * 16) OUO_TRY((launch_bwd_vec<256, 2>(a, grid, s)));
+    else if (n <= 512 * 16)
+      OUO_TRY((vec ? launch_bwd_vec<512, 2> : launch_bwd_elem<512, 2>)(a, grid, s));
     else {
       rms_bwd_long_kernel<<<grid, 512, 0, s>>>(a);
       OUO_CHECK_LAUNCH();

@@ -52,17 +52,18 @@ quant_rows_kernel(const __grid_constant__ QuantArgs a) {
     if (t == 0) a.scale[g][r] = 0.f;
     return;
   }
-  const char* x = reinterpret_cast<const char*>(a.X[g]) + r * a.ldx[g] * (a.bf16 ? 2 : 4);
+  constexpr int kBf = MODE == 1 || MODE == 3;
+  const char* x = reinterpret_cast<const char*>(a.X[g]) + r * a.ldx[g] * (kBf ? 2 : 4);
   RowRaw<TPR, NV, MODE> raw;
   float v[NV][8];
-  raw.load(x, t, n, a.bf16, a.vecx[g]);
+  raw.load(x, t, n, kBf, MODE <= 2);
   raw.get(v);
   float m = 0.f;
 #pragma unroll
   for (int c = 0; c < NV; ++c)
 #pragma unroll
     for (int i = 0; i < 8; ++i) m = max_mag(m, v[c][i]);
-  const Quant q = quant_of<MODE == 1 || MODE == 3>(team_max<TPR>(__float_as_uint(m), red));
+  const Quant q = quant_of<kBf>(team_max<TPR>(__float_as_uint(m), red));
   if (t == 0) a.scale[g][r] = q.scale;
   int8_t* o = a.Q[g] + r * a.ldq[g];
   store_q<TPR, NV, MODE>(o, t, n, a.vecq[g], v, q);
@@ -286,7 +287,7 @@ quant_cols_kernel(const __grid_constant__ QuantTArgs a) {
 
 template <int BF>
 int quant_cols(const ouo_mat& X, const ouo_mat& Q, float* scale, cudaStream_t s) {
-  // shared memory for two CTAs a SM; below 256 rows a CTA the cluster shrinks
+  // shared memory for two CTAs a SM; a CTA keeps 128 rows at least
   constexpr int kCached = 1600;
   constexpr size_t kSmem = (size_t)kCached * kSegBytes;
   static Once once;
@@ -593,12 +594,13 @@ int quant_rows(QuantArgs& a, int64_t rows, int64_t longest, int kind, cudaStream
   // (element by element too, a quantized row is one load and one store: the
   // smaller teams of the vector modes do better)
   const Team t = team_for(rows, longest, a.bf16 ? 1 : 2);
-  const int mode = (a.bf16 ? 1 : 2) + (kind == kRowsElem ? 2 : 0);
-  return with_team(t, mode, [&](auto tpr, auto nv, auto md) -> int {
+  return with_team_of(t, [&](auto tpr, auto nv) -> int {
     constexpr int TPR = decltype(tpr)::value, NV = decltype(nv)::value;
-    constexpr int MODE = decltype(md)::value;
     constexpr int kTeams = kTeamThreads<TPR> / TPR;
-    quant_rows_kernel<TPR, NV, MODE><<<(unsigned)ceil_div(rows, (int64_t)kTeams), kTeamThreads<TPR>, 0, s>>>(a);
+    auto kern = kind == kRowsElem
+                    ? (a.bf16 ? quant_rows_kernel<TPR, NV, 3> : quant_rows_kernel<TPR, NV, 4>)
+                    : (a.bf16 ? quant_rows_kernel<TPR, NV, 1> : quant_rows_kernel<TPR, NV, 2>);
+    kern<<<(unsigned)ceil_div(rows, (int64_t)kTeams), kTeamThreads<TPR>, 0, s>>>(a);
     OUO_CHECK_LAUNCH();
     return OUO_OK;
   });

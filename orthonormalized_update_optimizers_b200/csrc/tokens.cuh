@@ -393,8 +393,12 @@ int with_team(Team t, int mode, F&& f) {
     switch (mode) {
       case 1: return f(tpr, nv, C<1>{});
       case 2: return f(tpr, nv, C<2>{});
-      case 3: return f(tpr, nv, C<3>{});
-      case 4: return f(tpr, nv, C<4>{});
+      case 3:
+      case 4:  // of the teams that team_for gives these
+        if constexpr (decltype(nv)::value == 1 || decltype(tpr)::value == 512)
+          return mode == 3 ? f(tpr, nv, C<3>{}) : f(tpr, nv, C<4>{});
+        return set_error(OUO_ERR_UNSUPPORTED, "no team of %d x %d takes single elements",
+                         decltype(tpr)::value, decltype(nv)::value);
       case 5: return f(tpr, nv, C<5>{});
       default: return f(tpr, nv, C<0>{});
     }
