@@ -192,6 +192,13 @@ struct BwdModes {
   static constexpr int kUnits = kU0 + kU1 + kU2;
 };
 
+// Blocks of the gradient that an SM holds at once, by the chunks of 8 columns
+// that a block takes: what the grid counts on, so the registers are bounded to it
+// (8000 x 4095 bf16: 153 us with a register too many, 90 with two blocks).
+constexpr int bwd_blocks(int chunks) {
+  return chunks <= 128 ? 7 : chunks <= 256 ? 4 : chunks <= 512 ? 2 : 1;
+}
+
 // A block of TPR threads takes rows b, b + grid, ...; every thread keeps the
 // same columns of all of them, so that its share of dw stays in registers and
 // leaves once, to row b of the partial sums.  In modes 1, 2 and 5 DEPTH rows of dY,
@@ -200,7 +207,8 @@ struct BwdModes {
 // would otherwise leave the memory idle (16384 x 4096 bf16: 180 us without, 87 us
 // with it and with 16 elements a thread; HBM-bound at 6.2 TB/s).
 template <int TPR, int NV, int MODE, int DEPTH>
-__global__ void __launch_bounds__(TPR) rms_bwd_kernel(const __grid_constant__ NormBwdArgs a) {
+__global__ void __launch_bounds__(TPR, bwd_blocks(TPR * NV))
+rms_bwd_kernel(const __grid_constant__ NormBwdArgs a) {
   __shared__ float red[2][TPR / 32];
   using M = BwdModes<MODE>;
   extern __shared__ __align__(16) uint4 ring[];  // [DEPTH][NV][dY, H, dH][TPR pieces a unit]
@@ -430,7 +438,7 @@ int launch_bwd_elem(const NormBwdArgs& a, unsigned grid, cudaStream_t s) {
 // device.
 int64_t bwd_parts(int64_t rows, int64_t cols) {
   if (rows > 0 && rows <= 8 && rows * cols <= 16384) return 1;
-  const int64_t most = 148 * (cols <= 128 * 8 ? 7 : cols <= 128 * 16 ? 4 : cols <= 256 * 16 ? 2 : 1);
+  const int64_t most = 148 * bwd_blocks((int)(cols < 8192 ? ceil_div(cols, (int64_t)8) : 1024));
   return rows < most ? rows : most;
 }
 
