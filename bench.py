@@ -58,13 +58,20 @@ def _args():
     ap.add_argument("--no-sweep", action="store_true",
                     help="skip the standard-vs-Gram crossover points of the JSON line")
     ap.add_argument("--cpu-sample-layers", type=int, default=1)
-    ap.add_argument("--micro", choices=["gram", "dion", "dion_set", "head8"], default=None,
+    ap.add_argument("--micro", choices=["gram", "dion", "dion_set", "head8", "tokens"], default=None,
                     help="one kernel-level case for profiling: Gram NS on --nb blocks "
                          "of --m x --n bf16, one Dion / Orth-Dion matrix --m x --n "
                          "at --rank (--mode colnorm|qr), the 8B-shaped set of "
-                         "--layers layers in one grouped Dion / Orth-Dion call, or "
+                         "--layers layers in one grouped Dion / Orth-Dion call, "
                          "one training step of an 8-bit --m x --n head on --tokens "
-                         "tokens against a teacher, Dion3 step included")
+                         "tokens against a teacher, Dion3 step included, or each "
+                         "token operator's call (the cases of perf/operators.py, or "
+                         "those given by --case)")
+    ap.add_argument("--case", action="append", default=None,
+                    help="with --micro tokens: a case of perf/operators.py as JSON, "
+                         "or the name of a listed one; may be repeated; \"stream\": "
+                         "\"f32\" makes a bf16 norm's residual stream fp32, "
+                         "\"unaligned\": true puts a product's rows off 16 bytes")
     ap.add_argument("--nb", type=int, default=32)
     ap.add_argument("--m", type=int, default=1792)
     ap.add_argument("--n", type=int, default=4096)
@@ -962,6 +969,71 @@ def head8_step(tokens, m, n, dev, k=32):
     return step, 6 * tokens * m * n
 
 
+def run_tokens(args):
+    """GPU time of the token operators' calls: a CUDA graph of calls over
+    several input sets (together larger than L2 where a call's bytes are not
+    tiny).  `us` is the median of six replays after a pause; `us_load` that of
+    0.7 s of replays, with the SM clock sampled meanwhile.  One JSON line per
+    case, against its floor: bytes at the measured HBM rate, or 8-bit
+    operations at twice the measured bf16 rate."""
+    import torch
+
+    import perf.operators as cases
+
+    cases.own = True
+    cases._values = lambda s: s["q"]  # the call alone, its bytes not turned into values
+    peaks = _peaks()
+    listed = {c["name"]: c for c in cases.listed()}
+    for c in args.case or list(listed):
+        c = listed.get(c) or json.loads(c)
+        w = cases.work(c)
+        sets = [cases.prepare(dict(c), i) for i in range(max(2, min(8, int(4e8 / w["bytes"]) + 1)))]
+        if c.get("stream") == "f32":
+            for s in sets:
+                s.update({k: s[k].float() for k in ("r", "h", "dh", "dx") if s.get(k) is not None})
+            w["bytes"] += 2 * c["rows"] * c["cols"] * (3 if c["op"] == "rms_bwd" else 2)
+        if c.get("unaligned"):
+            for s in sets:
+                for k in ("a", "b"):
+                    odd = torch.empty((s[k].shape[0], c["k"] + 1), dtype=torch.int8, device="cuda")
+                    s[k] = odd[:, 1:].copy_(s[k])
+        for s in sets:
+            cases.run(s)
+        torch.cuda.synchronize()
+        floor = w["bytes"] / peaks["hbm_gbs"] / 1e3
+        if c["op"] == "mm":
+            floor = max(floor, w["flops"] / peaks["bf16_tflops"] / 2e6)
+        calls = len(sets) * max(1, min(10, int(500 / max(floor, 5)) // len(sets)))
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            for i in range(calls):
+                cases.run(sets[i % len(sets)])
+
+        def replays(n):
+            ev = [torch.cuda.Event(enable_timing=True) for _ in range(n + 1)]
+            ev[0].record()
+            for e in ev[1:]:
+                graph.replay()
+                e.record()
+            torch.cuda.synchronize()
+            return [a.elapsed_time(b) * 1e3 / calls for a, b in zip(ev, ev[1:])]
+
+        replays(1)
+        time.sleep(0.3)
+        us = statistics.median(replays(6))
+        sampler, load, t0 = ClockSampler(0), [], time.time()
+        sampler.start()
+        while len(load) < 8 or time.time() - t0 < 0.9:
+            load += replays(8)
+        print(json.dumps({"mode": "micro", "case": c, "us": round(us, 2),
+                          "floor_us": round(floor, 2), "of_floor": round(floor / us, 3),
+                          "gbs": round(w["bytes"] / us / 1e3, 0),
+                          "us_load": round(statistics.median(load[len(load) // 4:]), 2),
+                          "input_sets": len(sets), "clocks": sampler.stop()}), flush=True)
+        del graph, sets
+        torch.cuda.empty_cache()
+
+
 def run_micro(args):
     """One kernel-level case (for ncu captures): W warm-up calls, then K
     calls timed with CUDA events; prints one JSON line."""
@@ -1049,6 +1121,9 @@ def run_micro(args):
 
 def main():
     args = _args()
+    if args.micro == "tokens":
+        run_tokens(args)
+        return
     if args.micro:
         run_micro(args)
         return

@@ -432,8 +432,9 @@ int dion_shard_update(const ouo_mat* M, const ouo_mat* Q_state,
  * 8-bit matrices hold signed integers, one byte each (`ld` in bytes).
  * An output must be apart from the inputs and the other outputs, unless a call
  * says that it may be an input itself (same pointer, type and pitch).  Overlap
- * is refused, also between columns of one wider matrix; not seen is only that of
- * two matrices with gaps between their rows and different pitches.
+ * is refused (in a batch, within each matrix's operands), also between columns
+ * of one wider matrix; not seen is that of two matrices with gaps between their
+ * rows and different pitches.
  */
 
 /*

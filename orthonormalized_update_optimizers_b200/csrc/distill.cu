@@ -219,7 +219,7 @@ __device__ __forceinline__ double ld_cluster(uint32_t addr, double) {
   return __hiloint2double(ptx::ld_cluster_int(addr + 4), ptx::ld_cluster_int(addr));
 }
 
-// Bound by HBM: 4096 x 131072 bf16 in 171 us, 6.3 TB/s (191 without the prefetch).
+// Bound by HBM: 4096 x 131072 bf16 in 171-175 us, 6.2 TB/s (191 without the prefetch).
 // One row per cluster: its CTAs divide the vocabulary and join their maxima
 // and sums through distributed shared memory (one CTA: no join).
 template <int BF, int TH, class SOFT>
@@ -357,7 +357,7 @@ distill_kernel(const __grid_constant__ DistillArgs a) {
 }
 
 // Every CTA writes one segment of one row.  Bound by HBM: 4096 x 131072 bf16 in
-// 359 us, 6.0 TB/s.
+// 361 us, 5.9 TB/s.
 template <int BF, int TH>
 __global__ void __launch_bounds__(TH, 1024 / TH)
 distill_bwd_kernel(const __grid_constant__ DistillArgs a, int64_t seg, int segs) {

@@ -7,12 +7,13 @@
 //     128 rows of A and half of B's rows); persistent, two accumulators in
 //     TMEM, so that a tile's epilogue (scales, rounding, store) runs under the
 //     next tile's products.  Bound by the tensor pipe: 8192 x 14336 x 4096 in
-//     326 us, 2.95 POP/s, the pipe 78% active at the clock the power limit leaves.
+//     333 us, 2.89 POP/s, the pipe 78% active (390 us under a long load, at the
+//     1.33 GHz that the power limit leaves).
 //   * split kernel: for few tokens, or outputs of few tiles.  128 rows of one
 //     operand x BN rows of the other per cluster; the cluster's CTAs split K,
 //     and join their 32-bit sums through distributed shared memory (integer
 //     sums: the same bits in any order).  Bound by reading the larger operand,
-//     and by some 4 us of set-up and join: 16 x 14336 x 4096 in 14.7 us.
+//     and by some 4 us of set-up and join: 16 x 14336 x 4096 in 14.2 us.
 // Matrices whose rows do not start on 16-byte boundaries cannot be read by the
 // TMA; they take a CUDA-core kernel (dp4a).
 // int8_matmul_deep, for depths whose sums leave 32 bits, cuts K into pieces that
@@ -30,7 +31,9 @@ namespace ouo {
 namespace {
 
 // CUDA cores: 64 x 64 tile per block, 32 bytes of K per step, 4 x 4 outputs
-// per thread, four products per dp4a.  Takes any row pitch and alignment.
+// per thread, four products per dp4a.  Takes any row pitch and alignment, byte
+// by byte: 333 x 1024 x 4096 in 181 us (8.3 on the tensor cores), 1 x 14336 x
+// 4096 in 209.
 // DEEP: 32-bit sums of kSimtPiece elements are added in 64 bits.
 constexpr int64_t kSimtPiece = OUO_INT8_MAX_DEPTH / 32 * 32;
 

@@ -31,8 +31,9 @@ __device__ __forceinline__ const char* row_of(const void* p, int64_t r, int64_t 
 
 // A team per row, h in registers (as the values that H's type holds): x and
 // the residual are read once, and nothing is read back.  Bound by HBM: 16384 x
-// 4096 bf16 with residual and 8-bit output in 71 us, 6.6 TB/s; with types asked
-// for at run time it was 92 us, bound by instructions.
+// 4096 bf16 with residual and 8-bit output in 71 us, 73 under a long load that
+// lowers the clock (6.6, 6.4 TB/s); with types asked for at run time it was 92
+// us, bound by instructions.
 template <int TPR, int NV, int MODE>
 __global__ void __launch_bounds__(kTeamThreads<TPR>) rms_kernel(const __grid_constant__ NormArgs a) {
   constexpr int kWarps = kTeamThreads<TPR> / 32, kTeams = kTeamThreads<TPR> / TPR;
@@ -117,7 +118,8 @@ __global__ void __launch_bounds__(kTeamThreads<TPR>) rms_kernel(const __grid_con
 }
 
 // Rows too long for registers: one block per row; h is read back (from H, or
-// from X when there is none) for each of the later passes.
+// from X when there is none) for each of the later passes.  2048 x 20000 bf16,
+// residual, 8 bits: 84 us, 3.4 TB/s of what it has to move.
 __global__ void __launch_bounds__(512) rms_long_kernel(const __grid_constant__ NormArgs a) {
   __shared__ uint32_t red[32];
   const int n = (int)a.cols;
@@ -204,8 +206,8 @@ constexpr int bwd_blocks(int chunks) {
 // leaves once, to row b of the partial sums.  In modes 1, 2 and 5 DEPTH rows of dY,
 // H and dH are on their way to shared memory (cp.async, to slots that only the
 // copying warp reads, so without block barriers), since the reduction of a row
-// would otherwise leave the memory idle (16384 x 4096 bf16: 180 us without, 87 us
-// with it and with 16 elements a thread; HBM-bound at 6.2 TB/s).
+// would otherwise leave the memory idle (16384 x 4096 bf16: 180 us without, 88 us
+// with it and with 16 elements a thread; HBM-bound at 6.1 TB/s).
 template <int TPR, int NV, int MODE, int DEPTH>
 __global__ void __launch_bounds__(TPR, bwd_blocks(TPR * NV))
 rms_bwd_kernel(const __grid_constant__ NormBwdArgs a) {
@@ -353,7 +355,8 @@ rms_bwd_kernel(const __grid_constant__ NormBwdArgs a) {
 }
 
 // Rows too long for registers: dw's shares stay in the partial sums, where
-// each thread adds to its own columns.
+// each thread adds to its own columns.  Bound by the latency of its single-
+// element accesses: 4096 x 16384 bf16 in 1.08 ms, 0.5 TB/s.
 __global__ void __launch_bounds__(512) rms_bwd_long_kernel(const __grid_constant__ NormBwdArgs a) {
   __shared__ uint32_t red[32];
   const int n = (int)a.cols;

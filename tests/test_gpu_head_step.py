@@ -2,6 +2,9 @@
 teacher (norm, products, distillation, gradients, Dion3 step): it runs, also
 with a vocabulary whose input gradient is a deep product, and moves the
 weight."""
+import json
+import types
+
 import pytest
 import torch
 
@@ -27,3 +30,13 @@ def test_head_step_runs(tokens, m, n):
     for _ in range(2):
         step()
     assert torch.isfinite(held["loss"]).all() and torch.isfinite(held["W"]).all()
+
+
+@pytest.mark.parametrize("case", [
+    dict(op="rms", rows=5, cols=64, dtype="bf16", residual=True, int8=True, stream="f32"),
+    dict(op="rms_bwd", rows=5, cols=64, dtype="bf16", stream="f32"),
+    dict(op="mm", m=5, n=16, k=64, dtype="bf16", unaligned=True)])
+def test_timing_of_a_call_runs(case, capsys):
+    bench.run_tokens(types.SimpleNamespace(case=[json.dumps(case)]))
+    line = json.loads(capsys.readouterr().out)
+    assert line["case"] == case and line["us"] > 0 and line["us_load"] > 0
